@@ -8,6 +8,15 @@ raises.
 
     Wq, Ws, g = pack_weights(W)                # W: fp32 [n, k] on cuda
     out = mm_bf16_fp4(A, Wq, Ws, g)            # A: bf16 [m, k] on cuda -> bf16 [m, n]
+
+8-bit products with a scale per block of 128, for any number of rows, and what follows an
+lm_head product:
+
+    Wq, Ws = pack_weights_fp8(W)               # W: fp32, bf16 or f16 [n, k] -> E4M3, fp32 scales
+    Aq, As = quantize_fp8(A)                   # A: fp32, bf16 or f16 [m, k] -> E4M3, fp32 scales
+    out = mm_fp8(Aq, As, Wq, Ws)               # bf16 [m, n] (or f16, fp32)
+    h = mm_fp8_gated(Aq, As, Gq, Gs, Uq, Us)   # silu(A G^T) * (A U^T)
+    lp = token_logprobs(logits, tokens, topk=5)
 """
 from __future__ import annotations
 
@@ -15,12 +24,14 @@ import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
 __all__ = [
     "FiError", "KIND_GEMV", "KIND_MMA", "TACTIC_DEFAULT", "make_tactic", "tactic_fields",
-    "pack_weights", "mm_bf16_fp4", "splitk_reduce", "resolve_tactic", "default_tactic",
+    "pack_weights", "mm_bf16_fp4", "splitk_reduce", "quantize_fp8", "pack_weights_fp8", "mm_fp8",
+    "mm_fp8_gated", "token_logprobs", "TokenLogprobs", "MAX_TOPK", "resolve_tactic", "default_tactic",
     "list_tactics", "workspace_bytes", "set_workspace", "last_error", "version", "library",
     "library_path", "get_device_error", "debug_set", "DEBUG_STALL_PRODUCER", "DEBUG_WAIT_TIMEOUT_NS",
 ]
@@ -33,6 +44,10 @@ KIND_MMA = 1
 TACTIC_DEFAULT = -1
 # output element types of fi_mm_bf16_fp4_out / fi_splitk_reduce_out
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+# element types of the 8-bit products' inputs and outputs and of the logits
+_DTYPES_ANY = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+FP8_BLOCK = 128  # k (and weight rows) per scale
+MAX_TOPK = 32    # FI_LOGPROBS_MAX_TOPK
 
 _STATUS = {0: "FI_OK", -1: "FI_ERR_INVALID_ARG", -2: "FI_ERR_UNSUPPORTED_SHAPE",
            -3: "FI_ERR_UNSUPPORTED_ARCH", -4: "FI_ERR_WORKSPACE", -5: "FI_ERR_CUDA"}
@@ -88,6 +103,12 @@ def library() -> ctypes.CDLL:
         lib.fi_splitk_reduce.argtypes = [vp, i64, i64, i64, vp, vp, vp]
         lib.fi_mm_bf16_fp4_out.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int, i64, i64, i64, i64, vp, sz, vp]
         lib.fi_splitk_reduce_out.argtypes = [vp, i64, i64, i64, vp, vp, ctypes.c_int, vp]
+        ci = ctypes.c_int
+        lib.fi_fp8_quantize.argtypes = [vp, ci, i64, i64, vp, vp, vp]
+        lib.fi_fp8_pack_weights.argtypes = [vp, ci, i64, i64, vp, vp, vp]
+        lib.fi_mm_fp8.argtypes = [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp]
+        lib.fi_mm_fp8_gated.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, vp]
+        lib.fi_token_logprobs.argtypes = [vp, ci, i64, i64, i64, vp, ci, vp, vp, vp, vp, vp, vp]
         lib.fi_resolve_tactic.argtypes = [i64, i64, i64, i64, ctypes.c_int, ctypes.POINTER(TacticInfo)]
         lib.fi_default_tactic.argtypes = [i64, i64, i64, ctypes.c_int]
         lib.fi_default_tactic.restype = i64
@@ -101,7 +122,8 @@ def library() -> ctypes.CDLL:
         lib.fi_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint)]
         lib.fi_debug_set.argtypes = [ctypes.c_int, i64]
         for name in ("fi_nvfp4_pack_weights", "fi_mm_bf16_fp4", "fi_mm_bf16_fp4_ex", "fi_mm_bf16_fp4_noalloc",
-                     "fi_splitk_reduce", "fi_mm_bf16_fp4_out", "fi_splitk_reduce_out",
+                     "fi_splitk_reduce", "fi_mm_bf16_fp4_out", "fi_splitk_reduce_out", "fi_fp8_quantize",
+                     "fi_fp8_pack_weights", "fi_mm_fp8", "fi_mm_fp8_gated", "fi_token_logprobs",
                      "fi_resolve_tactic", "fi_list_tactics", "fi_set_workspace", "fi_version",
                      "fi_get_device_error", "fi_debug_set"):
             getattr(lib, name).restype = ctypes.c_int
@@ -339,3 +361,147 @@ def splitk_reduce(partials: torch.Tensor, gscale: torch.Tensor, out: torch.Tenso
         _check(library().fi_splitk_reduce_out(partials.data_ptr(), S, m, n, gscale.data_ptr(), out.data_ptr(),
                                               _DTYPES[dtype], _stream(partials.device)), "fi_splitk_reduce_out")
     return out
+
+
+# --------------------------------------------- 8-bit products, a scale per block of 128
+
+def _on(device: torch.device):
+    """The library works on the current device: switch only when the operands are on another."""
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _quantize(x: torch.Tensor, name: str, square: bool, out: tuple | None):
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES_ANY:
+        raise ValueError(f"{name} must be a bf16, f16 or fp32 tensor")
+    _require(x, name, x.dtype, 2)
+    rows, k = x.shape
+    shape = (-(-rows // FP8_BLOCK) if square else rows, -(-k // FP8_BLOCK))
+    dev = x.device
+    if out is None:
+        q = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=dev)
+        s = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        if len(out) != 2:
+            raise ValueError("out must be (codes, scale)")
+        q, s = out
+        _require(q, "codes", torch.float8_e4m3fn, 2)
+        _require(s, "scale", torch.float32, 2)
+        if tuple(q.shape) != (rows, k) or tuple(s.shape) != shape:
+            raise ValueError(f"codes must be [{rows}, {k}] and scale {list(shape)}, got {list(q.shape)} and "
+                             f"{list(s.shape)}")
+        _same_device(x, codes=q, scale=s)
+    lib = library()
+    fn = lib.fi_fp8_pack_weights if square else lib.fi_fp8_quantize
+    with _on(dev):
+        st = fn(x.data_ptr(), _DTYPES_ANY[x.dtype], rows, k, q.data_ptr(), s.data_ptr(), _stream(dev))
+        if st:
+            _check(st, "fi_fp8_pack_weights" if square else "fi_fp8_quantize")
+    return q, s
+
+
+def quantize_fp8(A: torch.Tensor, out: tuple | None = None):
+    """Activations A [m, k] (bf16, f16 or fp32, CUDA) -> (E4M3 codes [m, k], fp32 scales
+    [m, ceil(k / 128)]): scale = amax / 448 per row and block of 128 k, code = E4M3(x / scale).
+    `out` takes the two tensors to write into. k must be a multiple of 16."""
+    return _quantize(A, "A", False, out)
+
+
+def pack_weights_fp8(W: torch.Tensor, out: tuple | None = None):
+    """Weights W [n, k] (bf16, f16 or fp32, CUDA) -> (E4M3 codes [n, k], fp32 scales
+    [ceil(n / 128), ceil(k / 128)]), one scale per 128 x 128 block. k must be a multiple of 16."""
+    return _quantize(W, "W", True, out)
+
+
+def _fp8_weight(A: torch.Tensor, q: torch.Tensor, s: torch.Tensor, qn: str, sn: str) -> int:
+    """n of a weight's codes [n, k] and scales, after checking them against the activations."""
+    _require(q, qn, torch.float8_e4m3fn, 2)
+    _require(s, sn, torch.float32, 2)
+    n, k = q.shape
+    if k != A.shape[1] or s.shape[0] != -(-n // FP8_BLOCK) or s.shape[1] != -(-k // FP8_BLOCK):
+        raise ValueError(f"shape mismatch: Aq {tuple(A.shape)}, {qn} {tuple(q.shape)}, {sn} {tuple(s.shape)}")
+    return n
+
+
+def _mm_fp8(where: str, Aq, Ascale, weights: tuple, names: tuple, out, out_dtype):
+    _require(Aq, "Aq", torch.float8_e4m3fn, 2)
+    _require(Ascale, "Ascale", torch.float32, 2)
+    m, k = Aq.shape
+    if Ascale.shape[0] != m or Ascale.shape[1] != -(-k // FP8_BLOCK):
+        raise ValueError(f"shape mismatch: Aq {tuple(Aq.shape)}, Ascale {tuple(Ascale.shape)}")
+    n = _fp8_weight(Aq, weights[0], weights[1], names[0], names[1])
+    if len(weights) == 4 and _fp8_weight(Aq, weights[2], weights[3], names[2], names[3]) != n:
+        raise ValueError(f"{names[0]} has {n} rows and {names[2]} {weights[2].shape[0]}")
+    dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
+    if dtype not in _DTYPES_ANY or (out_dtype is not None and out_dtype != dtype):
+        raise ValueError(f"the output is bf16, f16 or fp32 (out_dtype {out_dtype}, out "
+                         f"{None if out is None else out.dtype})")
+    dev = Aq.device
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=dev)
+    else:
+        _require(out, "out", dtype, 2)
+        if tuple(out.shape) != (m, n):
+            raise ValueError(f"out must be [{m}, {n}], got {tuple(out.shape)}")
+    _same_device(Aq, Ascale=Ascale, out=out, **dict(zip(names, weights)))
+    with _on(dev):
+        st = getattr(library(), where)(Aq.data_ptr(), Ascale.data_ptr(), *[w.data_ptr() for w in weights],
+                                       out.data_ptr(), _DTYPES_ANY[dtype], m, n, k, _stream(dev))
+        if st:
+            _check(st, where)
+    return out
+
+
+def mm_fp8(Aq: torch.Tensor, Ascale: torch.Tensor, Wq: torch.Tensor, Wscale: torch.Tensor,
+           out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """out[m, n] = (Aq scaled by Ascale) . (Wq scaled by Wscale)^T for codes and scales of
+    quantize_fp8 and pack_weights_fp8; fp32 sums, bf16 out unless out_dtype (or the dtype of
+    `out`) is torch.float16 or torch.float32. Any m; k a multiple of 16."""
+    return _mm_fp8("fi_mm_fp8", Aq, Ascale, (Wq, Wscale), ("Wq", "Wscale"), out, out_dtype)
+
+
+def mm_fp8_gated(Aq: torch.Tensor, Ascale: torch.Tensor, Gq: torch.Tensor, Gscale: torch.Tensor,
+                 Uq: torch.Tensor, Uscale: torch.Tensor, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """silu(A G^T) * (A U^T) [m, n] in one kernel, both products as mm_fp8 computes them and not
+    rounded before the activation. G and U are [n, k]; of a fused [2n, k] weight with n a multiple
+    of 128, pass the two halves of its codes and scales."""
+    return _mm_fp8("fi_mm_fp8_gated", Aq, Ascale, (Gq, Gscale, Uq, Uscale), ("Gq", "Gscale", "Uq", "Uscale"),
+                   out, out_dtype)
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: torch.Tensor       # fp32 [rows]
+    entropy: torch.Tensor       # fp32 [rows]
+    rank: torch.Tensor          # int64 [rows], 0 for the greatest logit
+    top_logprobs: torch.Tensor  # fp32 [rows, min(topk, vocab)]
+    top_ids: torch.Tensor       # int64 [rows, min(topk, vocab)]
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, topk: int = 0) -> TokenLogprobs:
+    """Log probability, entropy, rank and the `topk` (at most MAX_TOPK) greatest alternatives of
+    one token per row: logits [rows, vocab] (bf16, f16 or fp32; rows may be further apart than
+    vocab, as in a padded lm_head), tokens int64 [rows]. Equal logits order by index; -inf entries
+    are masked; a token outside the vocabulary has logprob NaN and rank -1."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in _DTYPES_ANY or logits.dim() != 2:
+        raise ValueError("logits must be a 2-d bf16, f16 or fp32 CUDA tensor")
+    _require(tokens, "tokens", torch.int64, 1)
+    rows, vocab = logits.shape
+    ld = logits.stride(0) if rows > 1 else vocab
+    if (vocab > 1 and logits.stride(1) != 1) or ld < vocab:
+        raise ValueError("the logits of a row must be adjacent and the rows must not overlap")
+    if tokens.shape[0] != rows:
+        raise ValueError(f"tokens must be [{rows}], got {tuple(tokens.shape)}")
+    _same_device(logits, tokens=tokens)
+    dev = logits.device
+    kk = max(0, min(topk, vocab))
+    f = torch.empty((rows * (2 + kk),), dtype=torch.float32, device=dev)
+    i = torch.empty((rows * (1 + kk),), dtype=torch.int64, device=dev)
+    lp, ent, top = f[:rows], f[rows:2 * rows], f[2 * rows:].view(rows, kk)
+    rank, ids = i[:rows], i[rows:].view(rows, kk)
+    with _on(dev):
+        st = library().fi_token_logprobs(logits.data_ptr(), _DTYPES_ANY[logits.dtype], rows, vocab, ld,
+                                         tokens.data_ptr(), topk, lp.data_ptr(), ent.data_ptr(), rank.data_ptr(),
+                                         top.data_ptr(), ids.data_ptr(), _stream(dev))
+        if st:
+            _check(st, "fi_token_logprobs")
+    return TokenLogprobs(lp, ent, rank, top, ids)

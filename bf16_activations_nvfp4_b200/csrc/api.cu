@@ -62,7 +62,7 @@ int device_sm_count() {
   return g_sms[dev];
 }
 
-static int check_arch() {
+int check_arch() {
   int dev = 0;
   const int rc = current_device(&dev);
   if (rc != FI_OK) return rc;
@@ -609,6 +609,15 @@ std::atomic<int> g_debug_stall_launches{0};
 // limit of every mbarrier wait inside the kernels
 std::atomic<uint64_t> g_wait_timeout_ns{1000000000ull};
 }  // namespace
+
+uint64_t wait_timeout_ns() { return g_wait_timeout_ns; }
+
+int take_debug_stall() {
+  int left = g_debug_stall_launches;
+  while (left > 0 && !g_debug_stall_launches.compare_exchange_weak(left, left - 1)) {
+  }
+  return left > 0 ? 1 : 0;
+}
 
 // ------------------------------------------------------------------ checks
 

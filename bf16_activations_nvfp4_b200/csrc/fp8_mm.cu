@@ -1,0 +1,441 @@
+// 8-bit products with a scale per block of 128 (sm_100a: tcgen05 + TMA + TMEM).
+//
+//   out[i][j] = sum_b As[i][b] * Ws[j / 128][b] * (sum over the 128 k of block b of A[i][k] W[j][k])
+//
+// and its gated form, silu(g) * u with g and u two such products of the same activations.
+//
+// The scales change every 128 k, so the tensor core sums one block of k at a time into a fresh
+// TMEM buffer and the epilogue warps add it, times the block's scale, to fp32 accumulators in
+// registers while the tensor core works on the next block.
+//
+// Here the weights are the MMA's M side (128 rows) and up to 256 activation rows its N side, so
+// a weight byte is read once per 256 rows and one row costs no more than 16. Roles of a CTA:
+//   warp 0    TMA producer: 128 x 128 weight tiles (two for the gated form) and N x 128
+//             activation tiles into a ring, 128-byte swizzled;
+//   warp 1    one thread issues the MMAs (four K = 32 steps per block) and the commits;
+//   warp 2    the scales: As * Ws of a block into a small ring, several blocks ahead;
+//   warps 3.. epilogue, one thread per weight row (two groups of four warps halve the columns,
+//             or take the gate and the up tile).
+// K splits are the CTAs of one cluster: their fp32 sums meet in distributed shared memory, where
+// each CTA adds a slice of the outputs in split order. No workspace, no atomics, one launch.
+//
+// Every wait is bounded (sync.cuh). On a timeout the roles stop, the producer and the MMA issuer
+// wait, bounded, for what they have in flight, and every thread still meets the barriers.
+#include <cstdint>
+#include <algorithm>
+#include <atomic>
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "sync.cuh"
+#include "tc.cuh"
+
+namespace fi {
+
+namespace {
+
+constexpr int kTileRows = 128;                     // weight rows per tile (the MMA's M)
+constexpr uint32_t kTileBytes = kTileRows * 128;   // a tile of one k block
+constexpr int kScaleSlots = 8;                     // blocks the scale warp may be ahead
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi0 = 3;
+constexpr int kMaxStages = 10;
+
+// The geometry of one instance: N activation rows per tile, one weight tile or two (gated).
+template <int N, bool GATED>
+struct Geo {
+  static constexpr int kTiles = GATED ? 2 : 1;
+  static constexpr int kEpiWarps = GATED || N > 64 ? 8 : 4;
+  static constexpr int kThreads = (kWarpEpi0 + kEpiWarps) * 32;
+  static constexpr int kCols = !GATED && N > 64 ? N / 2 : N;  // accumulators per epilogue thread
+  static constexpr uint32_t kStageBytes = kTiles * kTileBytes + N * 128;
+  static constexpr int kCtas = (GATED ? N <= 32 : N <= 64) ? 2 : 1;  // resident per SM
+  static constexpr int kTmemCols = 512 / kCtas < kTiles * N * 4 ? 512 / kCtas : kTiles * N * 4;
+  static constexpr int kBufs = kTmemCols / (kTiles * N);  // blocks the tensor core may be ahead
+  static constexpr uint32_t kBudget = kCtas == 2 ? 112 * 1024 : 226 * 1024;
+  static constexpr uint32_t kScaleBytes = kScaleSlots * kTiles * N * 4;
+  static constexpr uint32_t kFixed = 1024 + kScaleBytes + (2 * kMaxStages + 2 * kBufs + 2 * kScaleSlots + 1) * 8 + 64;
+  static constexpr int kStages =
+      (kBudget - kFixed) / kStageBytes < kMaxStages ? (kBudget - kFixed) / kStageBytes : kMaxStages;
+  static constexpr uint32_t kRing = kStages * kStageBytes;
+  static constexpr uint32_t kSmem = kFixed + kRing;
+  static_assert(kStages >= 3, "ring");
+  static_assert(kBufs >= 2 && kBufs * kTiles * N <= 512, "TMEM");
+  static_assert((uint32_t)(kTiles * N) * kTileRows * 4 <= kRing, "the split sums reuse the ring");
+};
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), E4M3 A and B (bits
+// 7-9, 10-12 = 0), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__device__ __forceinline__ constexpr uint32_t f8_idesc(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// fp32 at `addr` (a shared-memory address of this CTA) in the cluster's CTA `rank`.
+__device__ __forceinline__ float ld_dsmem(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));
+  return v;
+}
+
+__device__ __forceinline__ void store_out(void* out, int dtype, int64_t at, float v) {
+  if (dtype == FI_DTYPE_F32)
+    static_cast<float*>(out)[at] = v;
+  else
+    static_cast<uint16_t*>(out)[at] = f32_to_out(v, dtype == FI_DTYPE_F16);
+}
+
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+template <int N, bool GATED>
+__global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
+    fp8_mm_kernel(const Fp8MmArgs p, const __grid_constant__ CUtensorMap tmap_a,
+                  const __grid_constant__ CUtensorMap tmap_w0, const __grid_constant__ CUtensorMap tmap_w1) {
+  using G = Geo<N, GATED>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ volatile int abort_flag;
+  __shared__ uint32_t tmem_slot;
+  const uint32_t raw_s = smem_addr(smem_raw);
+  const uint32_t base = (raw_s + 1023u) & ~1023u;
+  uint8_t* const basep = smem_raw + (base - raw_s);
+  float* const scales = reinterpret_cast<float*>(basep + G::kRing);  // [slot][tile][N]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(basep + G::kRing + G::kScaleBytes);
+  uint64_t* const empty = full + G::kStages;
+  uint64_t* const tmem_full = empty + G::kStages;
+  uint64_t* const tmem_empty = tmem_full + G::kBufs;
+  uint64_t* const scale_full = tmem_empty + G::kBufs;
+  uint64_t* const scale_empty = scale_full + kScaleSlots;
+  uint64_t* const drain = scale_empty + kScaleSlots;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.splits;
+  const int split = (int)(blockIdx.x % (unsigned)S);
+  const int64_t unit = blockIdx.x / (unsigned)S;
+  const int64_t tile_n = unit / p.tiles_m;
+  const int64_t m0 = (unit - tile_n * p.tiles_m) * N;
+  const int kb0 = (int)((int64_t)split * p.kblocks / S);
+  const int KB = (int)((int64_t)(split + 1) * p.kblocks / S) - kb0;
+  const int rows = (int)min((int64_t)N, p.m - m0);  // activation rows of this tile
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < G::kBufs; ++i) {
+      mbar_init(&tmem_full[i], 1);
+      mbar_init(&tmem_empty[i], G::kEpiWarps);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&scale_full[i], 1);
+      mbar_init(&scale_empty[i], G::kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+                 "r"((uint32_t)G::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();
+
+  if (warp == kWarpTma) {
+    if (lane == 0) {
+      pdl_wait();
+      int issued = 0;
+      for (int i = 0; i < KB && !p.debug_stall; ++i) {
+        const int st = i % G::kStages;
+        if (i >= G::kStages &&
+            !mbar_wait_bounded(&empty[st], ((i / G::kStages) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u))
+          break;
+        const uint32_t dst = base + (uint32_t)st * G::kStageBytes;
+        const int x = (kb0 + i) * kFp8Block;
+        mbar_arrive_expect_tx(&full[st], G::kStageBytes);
+        tma_load_2d(dst, &tmap_w0, x, (int)(tile_n * kTileRows), smem_addr(&full[st]));
+        if (GATED) tma_load_2d(dst + kTileBytes, &tmap_w1, x, (int)(tile_n * kTileRows), smem_addr(&full[st]));
+        tma_load_2d(dst + G::kTiles * kTileBytes, &tmap_a, x, (int)m0, smem_addr(&full[st]));
+        issued = i + 1;
+      }
+      // the copies in flight land before the CTA's shared memory is given up
+      volatile int never = 0;
+      for (int i = max(0, issued - G::kStages); i < issued; ++i)
+        mbar_wait_bounded(&full[i % G::kStages], (i / G::kStages) & 1, &never, p.timeout_ns, p.err, 4u);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = f8_idesc(kTileRows, N);
+      bool ok = true;
+      for (int i = 0; i < KB; ++i) {
+        const int st = i % G::kStages, b = i % G::kBufs;
+        ok = mbar_wait_bounded(&full[st], (i / G::kStages) & 1, &abort_flag, p.timeout_ns, p.err, 1u) &&
+             (i < G::kBufs ||
+              mbar_wait_bounded(&tmem_empty[b], ((i / G::kBufs) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 1u));
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t stage = base + (uint32_t)st * G::kStageBytes;
+        const uint64_t bdesc = sw128_desc(stage + G::kTiles * kTileBytes);
+#pragma unroll
+        for (int t = 0; t < G::kTiles; ++t) {
+          const uint64_t adesc = sw128_desc(stage + t * kTileBytes);
+          const uint32_t d = tmem + (uint32_t)((b * G::kTiles + t) * N);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)  // K = 32 bytes each
+            umma_f8(d, adesc + (uint64_t)(2 * s), bdesc + (uint64_t)(2 * s), idesc, s > 0);
+        }
+        umma_commit(&empty[st]);
+        umma_commit(&tmem_full[b]);
+      }
+      if (!ok) {  // the MMAs in flight end before TMEM is freed
+        volatile int never = 0;
+        umma_commit(drain);
+        mbar_wait_bounded(drain, 0, &never, p.timeout_ns, p.err, 8u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpScale) {
+    pdl_wait();
+    constexpr int kPer = (N + 31) / 32, kAhead = 4;
+    float sa[kAhead][kPer], sw[kAhead][G::kTiles];
+    auto load = [&](int i, int d) {
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) {
+        const int row = lane + 32 * r;
+        sa[d][r] = i < KB && row < rows ? __ldg(p.As + (m0 + row) * p.kblocks + kb0 + i) : 0.0f;
+      }
+#pragma unroll
+      for (int t = 0; t < G::kTiles; ++t)
+        sw[d][t] = i < KB ? __ldg(p.Ws[t] + tile_n * p.kblocks + kb0 + i) : 0.0f;
+    };
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) load(d, d);
+    bool ok = true;
+    for (int i0 = 0; i0 < KB && ok; i0 += kAhead) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        const int i = i0 + d;
+        if (i < KB && ok) {
+          const int sl = i % kScaleSlots;
+          if (i >= kScaleSlots)
+            ok = mbar_wait_bounded(&scale_empty[sl], ((i / kScaleSlots) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            float* dst = scales + sl * (G::kTiles * N);
+#pragma unroll
+            for (int t = 0; t < G::kTiles; ++t)
+#pragma unroll
+              for (int r = 0; r < kPer; ++r)
+                if (lane + 32 * r < N) dst[t * N + lane + 32 * r] = sa[d][r] * sw[d][t];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&scale_full[sl]);
+            load(i + kAhead, d);
+          }
+        }
+      }
+    }
+  } else {
+    const int epi = warp - kWarpEpi0, quarter = warp & 3, group = epi >> 2;
+    const int tile = GATED ? group : 0;
+    const int c0 = GATED ? 0 : group * G::kCols;  // first activation row (column) of this thread
+    const int wrow = quarter * 32 + lane;         // weight row in the tile
+    float acc[G::kCols];
+#pragma unroll
+    for (int c = 0; c < G::kCols; ++c) acc[c] = 0.0f;
+    bool ok = true;
+    for (int i = 0; i < KB; ++i) {
+      const int b = i % G::kBufs, sl = i % kScaleSlots;
+      ok = mbar_wait_bounded(&scale_full[sl], (i / kScaleSlots) & 1, &abort_flag, p.timeout_ns, p.err, 16u) &&
+           mbar_wait_bounded(&tmem_full[b], (i / G::kBufs) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)((b * G::kTiles + tile) * N + c0);
+      const float4* sp = reinterpret_cast<const float4*>(scales + sl * (G::kTiles * N) + tile * N + c0);
+#pragma unroll
+      for (int c = 0; c < G::kCols; c += 16) {
+        uint32_t d[16];
+        tmem_ld16_async(taddr + c, d);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 s4 = sp[c / 4 + q];
+          acc[c + 4 * q] = fmaf(__uint_as_float(d[4 * q]), s4.x, acc[c + 4 * q]);
+          acc[c + 4 * q + 1] = fmaf(__uint_as_float(d[4 * q + 1]), s4.y, acc[c + 4 * q + 1]);
+          acc[c + 4 * q + 2] = fmaf(__uint_as_float(d[4 * q + 2]), s4.z, acc[c + 4 * q + 2]);
+          acc[c + 4 * q + 3] = fmaf(__uint_as_float(d[4 * q + 3]), s4.w, acc[c + 4 * q + 3]);
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&tmem_empty[b]);
+        mbar_arrive(&scale_empty[sl]);
+      }
+    }
+    if (ok) {
+      if (!GATED && S == 1) {
+        const int64_t j = tile_n * kTileRows + wrow;
+        if (j < p.n) {
+#pragma unroll
+          for (int c = 0; c < G::kCols; ++c)
+            if (c0 + c < rows) store_out(p.out, p.out_dtype, (m0 + c0 + c) * p.n + j, acc[c]);
+        }
+      } else {
+        // the ring is free: every copy has landed and every MMA has read its operands
+        float* part = reinterpret_cast<float*>(basep) + (tile * N + c0) * kTileRows + wrow;
+#pragma unroll
+        for (int c = 0; c < G::kCols; ++c)
+          if (c0 + c < rows) part[c * kTileRows] = acc[c];
+      }
+    }
+  }
+
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  if (GATED || S > 1) {
+    __syncwarp();
+    cluster_sync();
+    const int total = rows * kTileRows;
+    const int chunk = ((total + S - 1) / S + 31) / 32 * 32;
+    const int e_end = min(total, (split + 1) * chunk);
+    for (int e = split * chunk + (int)threadIdx.x; e < e_end; e += G::kThreads) {
+      const int64_t j = tile_n * kTileRows + (e & (kTileRows - 1));
+      float v[G::kTiles];
+#pragma unroll
+      for (int t = 0; t < G::kTiles; ++t) {
+        const uint32_t a = base + (uint32_t)(t * N * kTileRows + e) * 4u;
+        v[t] = ld_dsmem(a, 0);
+        for (int r = 1; r < S; ++r) v[t] = __fadd_rn(v[t], ld_dsmem(a, (uint32_t)r));
+      }
+      if (j < p.n) store_out(p.out, p.out_dtype, (m0 + e / kTileRows) * p.n + j, GATED ? silu(v[0]) * v[G::kTiles - 1] : v[0]);
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its sums
+  } else {
+    __syncthreads();
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)G::kTmemCols)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------- host side
+
+int encode_codes(CUtensorMap* map, const uint8_t* base, int64_t k, int64_t rows, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)k, (uint64_t)rows};
+  const uint64_t strides[1] = {(uint64_t)k};
+  const uint32_t box[2] = {(uint32_t)kFp8Block, (uint32_t)box_rows};
+  return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int N, bool GATED>
+int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
+  using G = Geo<N, GATED>;
+  const int sms = device_sm_count();
+  const int64_t tiles_n = (a.n + kTileRows - 1) / kTileRows;
+  a.tiles_m = (int)((a.m + N - 1) / N);
+  const int64_t units = tiles_n * a.tiles_m;
+  // the split of least cost: waves of CTAs, each of its blocks of k and a start and an end worth
+  // about 6 of them, and 4 for the meeting of a cluster
+  const int64_t slots = (int64_t)sms * G::kCtas;
+  int64_t best = -1;
+  a.splits = 1;
+  for (int s = 1; s <= 8 && s <= a.kblocks; s *= 2) {
+    const int64_t cost = ((units * s + slots - 1) / slots) * ((a.kblocks + s - 1) / s + 6) + (s > 1 ? 4 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a.splits = s;
+    }
+  }
+  const int64_t grid = units * a.splits;
+  if (grid > 0x7fffffffLL || a.n > 0x7fffff00LL || a.m > 0x7fffff00LL || a.k > 0x7fffff00LL)
+    return set_error(FI_ERR_UNSUPPORTED_SHAPE, "m=%lld n=%lld k=%lld is too large", (long long)a.m, (long long)a.n,
+                     (long long)a.k);
+  CUtensorMap ta, tw[2];
+  int rc = encode_codes(&ta, a.A, a.k, a.m, N);
+  for (int t = 0; t < G::kTiles && rc == FI_OK; ++t) rc = encode_codes(&tw[t], a.W[t], a.k, a.n, kTileRows);
+  if (rc != FI_OK) return rc;
+  if (!GATED) tw[1] = tw[0];
+  auto kern = fp8_mm_kernel<N, GATED>;
+  static std::atomic<bool> configured[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return set_cuda_error("cudaGetDevice");
+  if (!configured[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem) != cudaSuccess)
+      return set_cuda_error("cudaFuncSetAttribute(fp8 smem)");
+    configured[dev] = true;
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = G::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, a, ta, tw[0], tw[1]) != cudaSuccess) return set_cuda_error("fp8_mm_kernel launch");
+  return FI_OK;
+}
+
+}  // namespace
+
+int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream) {
+  a.err = device_error_word();
+  if (!a.err) return set_cuda_error("cudaGetSymbolAddress(device error word)");
+  a.timeout_ns = wait_timeout_ns();
+  a.debug_stall = take_debug_stall();
+  if (gated) {
+    if (a.m <= 16) return launch_tile<16, true>(a, stream);
+    if (a.m <= 32) return launch_tile<32, true>(a, stream);
+    if (a.m <= 64) return launch_tile<64, true>(a, stream);
+    return launch_tile<128, true>(a, stream);
+  }
+  if (a.m <= 16) return launch_tile<16, false>(a, stream);
+  if (a.m <= 32) return launch_tile<32, false>(a, stream);
+  if (a.m <= 64) return launch_tile<64, false>(a, stream);
+  if (a.m <= 128) return launch_tile<128, false>(a, stream);
+  return launch_tile<256, false>(a, stream);
+}
+
+}  // namespace fi

@@ -17,6 +17,14 @@ int set_error(int status, const char* fmt, ...);
 int set_cuda_error(const char* what);  // reads and clears cudaGetLastError()
 void clear_error();
 
+// FI_OK when the current device is compute capability 10.0, else an error status.
+int check_arch();
+
+// Test hooks of fi_debug_set: the limit of every mbarrier wait, and whether the next launch's
+// producers stall (counts one launch down).
+uint64_t wait_timeout_ns();
+int take_debug_stall();
+
 // SM count of the current device (cached per device).
 int device_sm_count();
 
@@ -170,6 +178,49 @@ unsigned* device_error_word();
 // ---------------------------------------------------------------------- reduce
 int launch_splitk_reduce(const float* partials, int splits, int64_t m, int64_t n,
                          const float* gscale, uint16_t* out, bool out_f16, bool pdl, cudaStream_t stream);
+
+// ------------------------------------------------------------- 8-bit block scales
+// Codes are E4M3 bytes; a scale covers kFp8Block consecutive k of one row (activations) or of
+// kFp8Block rows (weights).
+constexpr int kFp8Block = 128;
+inline int64_t fp8_blocks(int64_t x) { return (x + kFp8Block - 1) / kFp8Block; }
+
+// x [rows, k] of element type `dtype` (fi_dtype) -> codes [rows, k] and scales: one per row and
+// block of k, or (square) one per block of rows and block of k.
+int launch_fp8_quantize(const void* x, int dtype, int64_t rows, int64_t k, bool square, uint8_t* q, float* scale,
+                        cudaStream_t stream);
+
+struct Fp8MmArgs {
+  const uint8_t* A;      // [m, k] codes
+  const float* As;       // [m, kblocks]
+  const uint8_t* W[2];   // [n, k] codes (gated: gate, up)
+  const float* Ws[2];    // [ceil(n / 128), kblocks]
+  void* out;             // [m, n] of out_dtype
+  int out_dtype;         // fi_dtype
+  int64_t m, n, k;
+  int kblocks;           // ceil(k / 128)
+  int splits;            // K splits: the CTAs of one cluster
+  int tiles_m;           // tiles along m
+  int debug_stall;       // test hook: the producer issues nothing (the waits time out)
+  unsigned* err;         // the device error word
+  uint64_t timeout_ns;   // limit of every mbarrier wait
+};
+int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream);
+
+// -------------------------------------------------------------- token log probabilities
+constexpr int kLogprobMaxTopk = 32;
+struct LogprobArgs {
+  const void* logits;  // [rows, vocab] of dtype, rows ld elements apart
+  int64_t rows, vocab, ld;
+  const int64_t* tokens;
+  int topk;            // min(topk, vocab) is written per row
+  float* logprob;
+  float* entropy;
+  int64_t* rank;
+  float* top_logprobs;
+  int64_t* top_ids;
+};
+int launch_token_logprobs(const LogprobArgs& a, int dtype, cudaStream_t stream);
 
 // ------------------------------------------------------------------------ pack
 int launch_pack(const float* W, int64_t n, int64_t k, uint8_t* Wq, uint8_t* Wscale,

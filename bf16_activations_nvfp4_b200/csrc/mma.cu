@@ -49,6 +49,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "sync.cuh"
+#include "tc.cuh"
 
 namespace fi {
 
@@ -69,26 +70,10 @@ constexpr uint32_t kWopBytes = kMmaTileRows * 128;  // 256 rows x 64 f16, 128-by
 // and one drain barrier per MMA-issuing thread
 constexpr int kNumBars = 2 * kRawStages + 3 * kMmaMaxOpStages + 3;
 
-// Shared-memory matrix descriptor of a K-major tile with 128-byte rows in the 128-byte swizzle
-// (8-row atoms of 1024 bytes): start address >> 4 in bits 0-13, leading-dimension offset 1
-// (unused for swizzled K-major), stride-dimension offset 1024 >> 4 in bits 32-45, descriptor
-// version 1 in bits 46-47, swizzle mode 2 (128 bytes) in bits 61-63.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-
 // Instruction descriptor of kind::f16: fp32 accumulator (bits 4-5 = 1), f16 A and B (bits 7-9,
 // 10-12 = 0), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
 __device__ __forceinline__ uint32_t f16_idesc(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
 }
 
 __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -120,11 +105,6 @@ __device__ __forceinline__ void tmem_st16_halves(uint32_t taddr, const uint32_t 
                  "r"(v[8 * q]), "r"(v[8 * q + 1]), "r"(v[8 * q + 2]), "r"(v[8 * q + 3]), "r"(v[8 * q + 4]),
                  "r"(v[8 * q + 5]), "r"(v[8 * q + 6]), "r"(v[8 * q + 7])
                  : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {

@@ -1,0 +1,33 @@
+// Tensor-core helpers shared by the tcgen05 kernels: operand descriptors, TMA tile loads and
+// commits.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+#include "sync.cuh"
+
+namespace fi {
+
+// Shared-memory matrix descriptor of a K-major tile with 128-byte rows in the 128-byte swizzle
+// (8-row atoms of 1024 bytes): start address >> 4 in bits 0-13, leading-dimension offset 1
+// (unused for swizzled K-major), stride-dimension offset 1024 >> 4 in bits 32-45, descriptor
+// version 1 in bits 46-47, swizzle mode 2 (128 bytes) in bits 61-63.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+}  // namespace fi

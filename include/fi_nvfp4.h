@@ -132,8 +132,9 @@ typedef struct {
 } fi_tactic_info;
 
 /* Output element types (the op writes bf16 by default; PR #4038's commits add an fp16 output
- * through the GEMV path, covered by its test of fp16 GEMV output). */
-typedef enum { FI_DTYPE_BF16 = 0, FI_DTYPE_F16 = 1 } fi_dtype;
+ * through the GEMV path, covered by its test of fp16 GEMV output). FI_DTYPE_F32 is taken by the
+ * 8-bit products and the token log probabilities only. */
+typedef enum { FI_DTYPE_BF16 = 0, FI_DTYPE_F16 = 1, FI_DTYPE_F32 = 2 } fi_dtype;
 
 /* ------------------------------------------------------------------ entry points */
 
@@ -261,6 +262,88 @@ FI_API int fi_splitk_reduce(const float* partials, int64_t splits, int64_t m, in
  * on); FI_ERR_INVALID_ARG for any other out_dtype. */
 FI_API int fi_splitk_reduce_out(const float* partials, int64_t splits, int64_t m, int64_t n,
                          const float* gscale, uint16_t* out, int out_dtype, fi_stream_t stream);
+
+/* ------------------------------------------------- 8-bit products, a scale per block of 128
+ *
+ * For the layers that are not held in 4 bits, and for any number of activation rows: E4M3 codes
+ * (the "FN" format: no infinities, largest value 448) with one fp32 scale per block of 128
+ * consecutive k. A scale of the activations covers one row (1 x 128), a scale of the weights 128
+ * rows (128 x 128). k must be a multiple of 16; where it is not one of 128 the last block is
+ * shorter, and so is the last block of weight rows. Codes are row-major and dense, scales too.
+ * None of these calls uses a workspace. Read and written only after the kernel that precedes the
+ * call on `stream` has completed (weights included).
+ */
+
+/*
+ * Activations to codes: for each row and block of k
+ *     scale = amax(|x|) / 448;  code = E4M3_rn_satfinite(x / scale), or 0 where scale == 0,
+ * two fp32 divisions, rounded to nearest even; bit-identical to a CPU implementation of the same
+ * steps. A NaN makes its block's scale and codes NaN; an infinity makes the scale infinite, its
+ * own code NaN and the finite codes of the block 0.
+ *   A       device [m, k] of `dtype` (any fi_dtype), 16-byte aligned.
+ *   Aq      device uint8 [m, k] (output), 16-byte aligned.
+ *   Ascale  device fp32 [m, ceil(k / 128)] (output).
+ * Preconditions: m >= 0, k >= 0, k % 16 == 0 (FI_ERR_UNSUPPORTED_SHAPE). m == 0 or k == 0 is a
+ * no-op.
+ */
+FI_API int fi_fp8_quantize(const void* A, int dtype, int64_t m, int64_t k, uint8_t* Aq, float* Ascale,
+                    fi_stream_t stream);
+
+/* Weights to codes: as fi_fp8_quantize, with one scale per 128 x 128 block: W [n, k] of `dtype`,
+ * Wq uint8 [n, k], Wscale fp32 [ceil(n / 128), ceil(k / 128)]. */
+FI_API int fi_fp8_pack_weights(const void* W, int dtype, int64_t n, int64_t k, uint8_t* Wq, float* Wscale,
+                        fi_stream_t stream);
+
+/*
+ * out[i][j] = round(sum_b Ascale[i][b] * Wscale[j / 128][b] * sum_{k in b} Aq[i][k] * Wq[j][k])
+ *
+ * The products of a block are exact and the tensor core sums them; the block sums, times the
+ * product of their two scales, are added in fp32 in order of k (K splits, where a call takes
+ * them, are added in order after that); one rounding to out_dtype (FI_DTYPE_BF16, FI_DTYPE_F16
+ * with +-inf from 65520 on, or FI_DTYPE_F32). Results repeat bit for bit from run to run. How many
+ * K splits a call takes depends on its sizes, so a row's last bits may depend on m.
+ *   Aq, Ascale  activations as written by fi_fp8_quantize; Aq 16-byte aligned.
+ *   Wq, Wscale  weights as written by fi_fp8_pack_weights; Wq 16-byte aligned.
+ *   out         device [m, n] of out_dtype; must not overlap the inputs.
+ * Preconditions: m, n, k >= 0, k % 16 == 0. m == 0 or n == 0 is a no-op; k == 0 writes zeros.
+ */
+FI_API int fi_mm_fp8(const uint8_t* Aq, const float* Ascale, const uint8_t* Wq, const float* Wscale, void* out,
+              int out_dtype, int64_t m, int64_t n, int64_t k, fi_stream_t stream);
+
+/*
+ * The first half of a gated feed-forward block in one kernel:
+ *     out[i][j] = round(g / (1 + exp(-g)) * u),   g = (A G^T)[i][j], u = (A U^T)[i][j]
+ * with g and u the fp32 sums of fi_mm_fp8, never rounded in between. G and U are two weights
+ * [n, k] with their scales (of a fused [2n, k] weight with n a multiple of 128, its two halves).
+ * Other arguments and preconditions are those of fi_mm_fp8.
+ */
+FI_API int fi_mm_fp8_gated(const uint8_t* Aq, const float* Ascale, const uint8_t* Gq, const float* Gscale,
+                    const uint8_t* Uq, const float* Uscale, void* out, int out_dtype, int64_t m,
+                    int64_t n, int64_t k, fi_stream_t stream);
+
+/* ------------------------------------------------------------ token log probabilities */
+
+/*
+ * What a server answers with after the lm_head product: per row z of logits (in fp32, natural
+ * logarithms),
+ *     logprob = z[token] - ln(sum exp(z)),   entropy = -sum p ln(p),
+ *     rank    = the number of entries before the token in the order (value descending, index
+ *               ascending): 0 for the first,
+ *     top     = the first topk entries of that order: their log probabilities and indices.
+ *   logits        device [rows, vocab] of `dtype` (any fi_dtype), rows `ld` >= vocab elements apart.
+ *   tokens        device int64 [rows].
+ *   logprob, entropy  device fp32 [rows] (outputs).
+ *   rank          device int64 [rows] (output).
+ *   top_logprobs, top_ids  device fp32 / int64 [rows, min(topk, vocab)] (outputs; unused if topk == 0).
+ * An entry of -inf is masked: it has probability 0 and adds nothing. A row of nothing else has
+ * logprob -inf and entropy 0. A row that holds NaN or +inf has NaN logprob and entropy; NaN comes
+ * first in the order. A token outside [0, vocab) has logprob NaN and rank -1.
+ * Preconditions: rows >= 0, vocab >= 1, 0 <= topk <= FI_LOGPROBS_MAX_TOPK. rows == 0 is a no-op.
+ */
+#define FI_LOGPROBS_MAX_TOPK 32
+FI_API int fi_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                      const int64_t* tokens, int topk, float* logprob, float* entropy, int64_t* rank,
+                      float* top_logprobs, int64_t* top_ids, fi_stream_t stream);
 
 /* --------------------------------------------------------------- host helpers
  * These run on the host only and never launch work. `num_sms` <= 0 means "query the
