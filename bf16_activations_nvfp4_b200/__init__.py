@@ -365,37 +365,47 @@ def splitk_reduce(partials: torch.Tensor, gscale: torch.Tensor, out: torch.Tenso
 
 # --------------------------------------------- 8-bit products, a scale per block of 128
 
-def _on(device: torch.device):
-    """The library works on the current device: switch only when the operands are on another."""
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+def _call(name: str, device: int, *args) -> None:
+    """library().name(*args, current stream of `device`), with that device current."""
+    fn = getattr(_lib or library(), name)
+    stream = torch._C._cuda_getCurrentRawStream(device)  # the handle alone: a Stream object costs 2 us
+    if device == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:  # the library works on the current device
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
+    if st:
+        _check(st, name)
 
 
-def _quantize(x: torch.Tensor, name: str, square: bool, out: tuple | None):
-    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES_ANY:
+def _is(t, dtype: torch.dtype, ndim: int) -> bool:
+    """What _require asks, without its message."""
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+
+
+def _quantize(where: str, x: torch.Tensor, name: str, square: bool, out: tuple | None):
+    dtype = x.dtype if isinstance(x, torch.Tensor) else None
+    if dtype not in _DTYPES_ANY:
         raise ValueError(f"{name} must be a bf16, f16 or fp32 tensor")
-    _require(x, name, x.dtype, 2)
+    if not _is(x, dtype, 2):
+        _require(x, name, dtype, 2)
     rows, k = x.shape
     shape = (-(-rows // FP8_BLOCK) if square else rows, -(-k // FP8_BLOCK))
-    dev = x.device
+    dev = x.get_device()
     if out is None:
-        q = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=dev)
-        s = torch.empty(shape, dtype=torch.float32, device=dev)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        s = torch.empty(shape, dtype=torch.float32, device=x.device)
     else:
         if len(out) != 2:
             raise ValueError("out must be (codes, scale)")
         q, s = out
         _require(q, "codes", torch.float8_e4m3fn, 2)
         _require(s, "scale", torch.float32, 2)
-        if tuple(q.shape) != (rows, k) or tuple(s.shape) != shape:
+        if q.shape != (rows, k) or s.shape != shape:
             raise ValueError(f"codes must be [{rows}, {k}] and scale {list(shape)}, got {list(q.shape)} and "
                              f"{list(s.shape)}")
         _same_device(x, codes=q, scale=s)
-    lib = library()
-    fn = lib.fi_fp8_pack_weights if square else lib.fi_fp8_quantize
-    with _on(dev):
-        st = fn(x.data_ptr(), _DTYPES_ANY[x.dtype], rows, k, q.data_ptr(), s.data_ptr(), _stream(dev))
-        if st:
-            _check(st, "fi_fp8_pack_weights" if square else "fi_fp8_quantize")
+    _call(where, dev, x.data_ptr(), _DTYPES_ANY[dtype], rows, k, q.data_ptr(), s.data_ptr())
     return q, s
 
 
@@ -403,52 +413,40 @@ def quantize_fp8(A: torch.Tensor, out: tuple | None = None):
     """Activations A [m, k] (bf16, f16 or fp32, CUDA) -> (E4M3 codes [m, k], fp32 scales
     [m, ceil(k / 128)]): scale = amax / 448 per row and block of 128 k, code = E4M3(x / scale).
     `out` takes the two tensors to write into. k must be a multiple of 16."""
-    return _quantize(A, "A", False, out)
+    return _quantize("fi_fp8_quantize", A, "A", False, out)
 
 
 def pack_weights_fp8(W: torch.Tensor, out: tuple | None = None):
     """Weights W [n, k] (bf16, f16 or fp32, CUDA) -> (E4M3 codes [n, k], fp32 scales
     [ceil(n / 128), ceil(k / 128)]), one scale per 128 x 128 block. k must be a multiple of 16."""
-    return _quantize(W, "W", True, out)
+    return _quantize("fi_fp8_pack_weights", W, "W", True, out)
 
 
-def _fp8_weight(A: torch.Tensor, q: torch.Tensor, s: torch.Tensor, qn: str, sn: str) -> int:
-    """n of a weight's codes [n, k] and scales, after checking them against the activations."""
-    _require(q, qn, torch.float8_e4m3fn, 2)
-    _require(s, sn, torch.float32, 2)
-    n, k = q.shape
-    if k != A.shape[1] or s.shape[0] != -(-n // FP8_BLOCK) or s.shape[1] != -(-k // FP8_BLOCK):
-        raise ValueError(f"shape mismatch: Aq {tuple(A.shape)}, {qn} {tuple(q.shape)}, {sn} {tuple(s.shape)}")
-    return n
+def _fp8_operand(q: torch.Tensor, s: torch.Tensor, k: int | None, rows: int, qn: str, sn: str) -> tuple:
+    """(rows, k) of a matrix of codes [r, k] and its scales, one per `rows` rows and block of k."""
+    if not (_is(q, torch.float8_e4m3fn, 2) and _is(s, torch.float32, 2)):
+        _require(q, qn, torch.float8_e4m3fn, 2)
+        _require(s, sn, torch.float32, 2)
+    r, kq = q.shape
+    sr, sk = s.shape
+    if (k is not None and kq != k) or sr != -(-r // rows) or sk != -(-kq // FP8_BLOCK):
+        raise ValueError(f"shape mismatch: {qn} {tuple(q.shape)}, {sn} {tuple(s.shape)}" +
+                         (f", k = {k}" if k is not None else ""))
+    return r, kq
 
 
-def _mm_fp8(where: str, Aq, Ascale, weights: tuple, names: tuple, out, out_dtype):
-    _require(Aq, "Aq", torch.float8_e4m3fn, 2)
-    _require(Ascale, "Ascale", torch.float32, 2)
-    m, k = Aq.shape
-    if Ascale.shape[0] != m or Ascale.shape[1] != -(-k // FP8_BLOCK):
-        raise ValueError(f"shape mismatch: Aq {tuple(Aq.shape)}, Ascale {tuple(Ascale.shape)}")
-    n = _fp8_weight(Aq, weights[0], weights[1], names[0], names[1])
-    if len(weights) == 4 and _fp8_weight(Aq, weights[2], weights[3], names[2], names[3]) != n:
-        raise ValueError(f"{names[0]} has {n} rows and {names[2]} {weights[2].shape[0]}")
+def _fp8_out(Aq: torch.Tensor, m: int, n: int, out: torch.Tensor | None, out_dtype: torch.dtype | None):
     dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
     if dtype not in _DTYPES_ANY or (out_dtype is not None and out_dtype != dtype):
         raise ValueError(f"the output is bf16, f16 or fp32 (out_dtype {out_dtype}, out "
                          f"{None if out is None else out.dtype})")
-    dev = Aq.device
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=dev)
-    else:
-        _require(out, "out", dtype, 2)
-        if tuple(out.shape) != (m, n):
-            raise ValueError(f"out must be [{m}, {n}], got {tuple(out.shape)}")
-    _same_device(Aq, Ascale=Ascale, out=out, **dict(zip(names, weights)))
-    with _on(dev):
-        st = getattr(library(), where)(Aq.data_ptr(), Ascale.data_ptr(), *[w.data_ptr() for w in weights],
-                                       out.data_ptr(), _DTYPES_ANY[dtype], m, n, k, _stream(dev))
-        if st:
-            _check(st, where)
-    return out
+        return torch.empty((m, n), dtype=dtype, device=Aq.device), dtype
+    _require(out, "out", dtype, 2)
+    if out.shape != (m, n):
+        raise ValueError(f"out must be [{m}, {n}], got {tuple(out.shape)}")
+    _same_device(Aq, out=out)
+    return out, dtype
 
 
 def mm_fp8(Aq: torch.Tensor, Ascale: torch.Tensor, Wq: torch.Tensor, Wscale: torch.Tensor,
@@ -456,7 +454,15 @@ def mm_fp8(Aq: torch.Tensor, Ascale: torch.Tensor, Wq: torch.Tensor, Wscale: tor
     """out[m, n] = (Aq scaled by Ascale) . (Wq scaled by Wscale)^T for codes and scales of
     quantize_fp8 and pack_weights_fp8; fp32 sums, bf16 out unless out_dtype (or the dtype of
     `out`) is torch.float16 or torch.float32. Any m; k a multiple of 16."""
-    return _mm_fp8("fi_mm_fp8", Aq, Ascale, (Wq, Wscale), ("Wq", "Wscale"), out, out_dtype)
+    m, k = _fp8_operand(Aq, Ascale, None, 1, "Aq", "Ascale")
+    n, _ = _fp8_operand(Wq, Wscale, k, FP8_BLOCK, "Wq", "Wscale")
+    dev = Aq.get_device()
+    if Ascale.get_device() != dev or Wq.get_device() != dev or Wscale.get_device() != dev:
+        _same_device(Aq, Ascale=Ascale, Wq=Wq, Wscale=Wscale)
+    out, dtype = _fp8_out(Aq, m, n, out, out_dtype)
+    _call("fi_mm_fp8", dev, Aq.data_ptr(), Ascale.data_ptr(), Wq.data_ptr(), Wscale.data_ptr(), out.data_ptr(),
+          _DTYPES_ANY[dtype], m, n, k)
+    return out
 
 
 def mm_fp8_gated(Aq: torch.Tensor, Ascale: torch.Tensor, Gq: torch.Tensor, Gscale: torch.Tensor,
@@ -465,8 +471,18 @@ def mm_fp8_gated(Aq: torch.Tensor, Ascale: torch.Tensor, Gq: torch.Tensor, Gscal
     """silu(A G^T) * (A U^T) [m, n] in one kernel, both products as mm_fp8 computes them and not
     rounded before the activation. G and U are [n, k]; of a fused [2n, k] weight with n a multiple
     of 128, pass the two halves of its codes and scales."""
-    return _mm_fp8("fi_mm_fp8_gated", Aq, Ascale, (Gq, Gscale, Uq, Uscale), ("Gq", "Gscale", "Uq", "Uscale"),
-                   out, out_dtype)
+    m, k = _fp8_operand(Aq, Ascale, None, 1, "Aq", "Ascale")
+    n, _ = _fp8_operand(Gq, Gscale, k, FP8_BLOCK, "Gq", "Gscale")
+    if _fp8_operand(Uq, Uscale, k, FP8_BLOCK, "Uq", "Uscale")[0] != n:
+        raise ValueError(f"Gq has {n} rows and Uq {Uq.shape[0]}")
+    dev = Aq.get_device()
+    for t in (Ascale, Gq, Gscale, Uq, Uscale):
+        if t.get_device() != dev:
+            _same_device(Aq, Ascale=Ascale, Gq=Gq, Gscale=Gscale, Uq=Uq, Uscale=Uscale)
+    out, dtype = _fp8_out(Aq, m, n, out, out_dtype)
+    _call("fi_mm_fp8_gated", dev, Aq.data_ptr(), Ascale.data_ptr(), Gq.data_ptr(), Gscale.data_ptr(), Uq.data_ptr(),
+          Uscale.data_ptr(), out.data_ptr(), _DTYPES_ANY[dtype], m, n, k)
+    return out
 
 
 class TokenLogprobs(NamedTuple):
@@ -484,24 +500,25 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, topk: int = 0) ->
     are masked; a token outside the vocabulary has logprob NaN and rank -1."""
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in _DTYPES_ANY or logits.dim() != 2:
         raise ValueError("logits must be a 2-d bf16, f16 or fp32 CUDA tensor")
-    _require(tokens, "tokens", torch.int64, 1)
+    if not _is(tokens, torch.int64, 1):
+        _require(tokens, "tokens", torch.int64, 1)
     rows, vocab = logits.shape
-    ld = logits.stride(0) if rows > 1 else vocab
-    if (vocab > 1 and logits.stride(1) != 1) or ld < vocab:
+    ld, inner = logits.stride()
+    if rows <= 1:
+        ld = vocab
+    if (vocab > 1 and inner != 1) or ld < vocab:
         raise ValueError("the logits of a row must be adjacent and the rows must not overlap")
     if tokens.shape[0] != rows:
         raise ValueError(f"tokens must be [{rows}], got {tuple(tokens.shape)}")
-    _same_device(logits, tokens=tokens)
-    dev = logits.device
+    dev = logits.get_device()
+    if tokens.get_device() != dev:
+        _same_device(logits, tokens=tokens)
     kk = max(0, min(topk, vocab))
-    f = torch.empty((rows * (2 + kk),), dtype=torch.float32, device=dev)
-    i = torch.empty((rows * (1 + kk),), dtype=torch.int64, device=dev)
-    lp, ent, top = f[:rows], f[rows:2 * rows], f[2 * rows:].view(rows, kk)
-    rank, ids = i[:rows], i[rows:].view(rows, kk)
-    with _on(dev):
-        st = library().fi_token_logprobs(logits.data_ptr(), _DTYPES_ANY[logits.dtype], rows, vocab, ld,
-                                         tokens.data_ptr(), topk, lp.data_ptr(), ent.data_ptr(), rank.data_ptr(),
-                                         top.data_ptr(), ids.data_ptr(), _stream(dev))
-        if st:
-            _check(st, "fi_token_logprobs")
+    device = logits.device
+    lp, ent = torch.empty((2, rows), dtype=torch.float32, device=device).unbind()
+    rank = torch.empty_like(tokens)
+    top = torch.empty((rows, kk), dtype=torch.float32, device=device)
+    ids = torch.empty_like(top, dtype=torch.int64)
+    _call("fi_token_logprobs", dev, logits.data_ptr(), _DTYPES_ANY[logits.dtype], rows, vocab, ld, tokens.data_ptr(),
+          topk, lp.data_ptr(), ent.data_ptr(), rank.data_ptr(), top.data_ptr(), ids.data_ptr())
     return TokenLogprobs(lp, ent, rank, top, ids)

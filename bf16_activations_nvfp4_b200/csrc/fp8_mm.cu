@@ -30,7 +30,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "sync.cuh"
-#include "tc.cuh"
+#include "fp8_tc.cuh"
 
 namespace fi {
 
@@ -64,54 +64,6 @@ struct Geo {
   static_assert(kBufs >= 2 && kBufs * kTiles * N <= 512, "TMEM");
   static_assert((uint32_t)(kTiles * N) * kTileRows * 4 <= kRing, "the split sums reuse the ring");
 };
-
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Instruction descriptor of kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), E4M3 A and B (bits
-// 7-9, 10-12 = 0), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
-__device__ __forceinline__ constexpr uint32_t f8_idesc(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// fp32 at `addr` (a shared-memory address of this CTA) in the cluster's CTA `rank`.
-__device__ __forceinline__ float ld_dsmem(uint32_t addr, uint32_t rank) {
-  uint32_t remote;
-  float v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));
-  return v;
-}
-
-__device__ __forceinline__ void store_out(void* out, int dtype, int64_t at, float v) {
-  if (dtype == FI_DTYPE_F32)
-    static_cast<float*>(out)[at] = v;
-  else
-    static_cast<uint16_t*>(out)[at] = f32_to_out(v, dtype == FI_DTYPE_F16);
-}
-
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 template <int N, bool GATED>
 __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
@@ -288,7 +240,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       for (int c = 0; c < G::kCols; c += 16) {
         uint32_t d[16];
         tmem_ld16_async(taddr + c, d);
-        tmem_wait_ld();
+        tmem_wait_ld(d);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 s4 = sp[c / 4 + q];
@@ -355,14 +307,6 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
 
 // ---------------------------------------------------------------------------- host side
 
-int encode_codes(CUtensorMap* map, const uint8_t* base, int64_t k, int64_t rows, int box_rows) {
-  const uint64_t dims[2] = {(uint64_t)k, (uint64_t)rows};
-  const uint64_t strides[1] = {(uint64_t)k};
-  const uint32_t box[2] = {(uint32_t)kFp8Block, (uint32_t)box_rows};
-  return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
-                           CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int N, bool GATED>
 int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
   using G = Geo<N, GATED>;
@@ -425,6 +369,7 @@ int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream) {
   if (!a.err) return set_cuda_error("cudaGetSymbolAddress(device error word)");
   a.timeout_ns = wait_timeout_ns();
   a.debug_stall = take_debug_stall();
+  if (a.m > 256) return launch_fp8_wide(a, gated, stream);
   if (gated) {
     if (a.m <= 16) return launch_tile<16, true>(a, stream);
     if (a.m <= 32) return launch_tile<32, true>(a, stream);

@@ -1,0 +1,517 @@
+// 8-bit products with a scale per block of 128 at prompt sizes (sm_100a: tcgen05 on CTA pairs).
+//
+// The same sums as fp8_mm.cu, for many activation rows, where the tensor cores are the bound. A
+// pair of CTAs (a cluster of 2) owns a tile of 256 activation rows x 256 weight rows, or of 256
+// activation rows x (128 gate + 128 up rows) in the gated form: one tcgen05.mma of both SMs reads
+// 128 rows of A from each CTA and 128 rows of B from each, so a CTA loads 32 KB per 128 k and
+// feeds 256 columns. Roles of a CTA (12 warps):
+//   warp 0      TMA producer of its 128 A rows and 128 B rows, a ring of 5 stages; the bytes of
+//               both CTAs complete one barrier, in the pair's first CTA;
+//   warp 1      in the first CTA, one thread issues the MMAs for both; the commits arrive in both;
+//   warp 2      the scales As * Ws of a block, several blocks ahead, into a small ring;
+//   warps 4-11  epilogue, one thread per activation row and half of the columns (128): a block's
+//               sums, times the row's scale, are added to 128 fp32 registers while the tensor
+//               cores fill the other TMEM buffer. setmaxnreg gives these warps 216 registers.
+// The CTAs are persistent: tiles go round-robin over the pairs, in groups of 8 along m, so that
+// the pairs at work share operand rows in L2; the next tile's blocks start while the last one's
+// outputs are written.
+//
+// Every wait is bounded; on a timeout the roles stop and every thread still meets the barriers.
+#include <cstdint>
+#include <algorithm>
+#include <atomic>
+
+#include "fp8_tc.cuh"
+
+namespace fi {
+
+namespace {
+
+constexpr int kStages = 5, kBufs = 2, kSlots = 8, kThreads = 384;
+constexpr int kRows = 128;                                      // activation rows of a CTA
+constexpr uint32_t kHalfBytes = kRows * 128, kStageBytes = 2 * kHalfBytes;
+constexpr uint32_t kPairBytes = 2 * kStageBytes;                // bytes a full barrier waits for
+constexpr uint32_t kOutBytes = 32 * 1024;                       // staging of the epilogue: 4 KB per warp
+constexpr uint32_t kScaleBytes = kSlots * 2 * kRows * 4;
+constexpr int kGroupM = 8;
+constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kScaleBytes + 256;
+constexpr int kEpiRegs = 216, kOtherRegs = 64;
+// registers after the split: the epilogue's two warpgroups and the other one stay within the launch's 168 a thread
+static_assert(256 * kEpiRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// This shared-memory address in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives on the barrier at this offset in both CTAs when the MMAs issued so far are complete.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// Arrives on a barrier of the pair. It orders TMEM reads only (a tcgen05 fence precedes it), so the
+// default scope is enough: with cluster scope each arrival is a memory barrier, and the kernel ran
+// at half its speed.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// (x, y) += (a, b) * s, both lanes of one packed instruction.
+__device__ __forceinline__ void fma_pair(float& x, float& y, uint32_t a, uint32_t b, float s) {
+  asm("{\n .reg .b64 d, e, f;\n mov.b64 d, {%2, %3};\n mov.b64 e, {%4, %4};\n mov.b64 f, {%0, %1};\n"
+      " fma.rn.f32x2 f, d, e, f;\n mov.b64 {%0, %1}, f;\n}"
+      : "+f"(x), "+f"(y)
+      : "r"(a), "r"(b), "f"(s));
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+struct WideArgs {
+  Fp8MmArgs p;
+  int tiles_n;        // tiles along n (256 columns, or 128 of the gated form)
+  int64_t tiles;      // tiles in all
+  int wide_stores;    // out rows take 16-byte stores
+};
+
+// The tile's (m, n) in units of tiles.
+__device__ __forceinline__ void tile_at(const WideArgs& w, int64_t t, int& tm, int& tn) {
+  const int64_t per = (int64_t)kGroupM * w.tiles_n;
+  const int g = (int)(t / per);
+  const int r = (int)(t - g * per);
+  const int gm = min(kGroupM, w.p.tiles_m - g * kGroupM);
+  tn = r / gm;
+  tm = g * kGroupM + (r - tn * gm);
+}
+
+// One warp's 32 rows x kCols columns of `acc` (from column C0 on) to out rows row0.., columns
+// col0..: through 4 KB of shared memory, so that a row's 128 bytes leave together.
+template <int C0, int kCols>
+__device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const float (&acc)[128], uint8_t* stage,
+                                           int lane, int64_t row0, int64_t col0) {
+  const bool f32 = p.out_dtype == FI_DTYPE_F32;
+  const int es = f32 ? 4 : 2;
+  const uint32_t sbase = smem_addr(stage);
+  uint8_t* const out = static_cast<uint8_t*>(p.out);
+  auto flush = [&](int64_t col, int per) {  // 128 bytes of each of the 32 rows, from `col` on; `per` elements per 16 bytes
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + lane / 8, ch = lane % 8;
+      uint4 v;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(sbase + (uint32_t)(r * 128 + ((ch ^ (r & 7)) * 16))));
+      const int64_t row = row0 + r, c = col + ch * per;
+      if (row < p.m && c < p.n) {
+        uint8_t* dst = out + (row * p.n + c) * es;
+        if (wide && c + per <= p.n) {
+          *reinterpret_cast<uint4*>(dst) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (e < per && c + e < p.n) {
+              if (f32)
+                reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
+              else
+                reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  };
+  auto put = [&](int ch, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     sbase + (uint32_t)(lane * 128 + ((ch ^ (lane & 7)) * 16))),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+  };
+  if (f32) {
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32) {
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) {
+        const float* a = acc + C0 + c + ch * 4;
+        put(ch, __float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
+      }
+      flush(col0 + c, 4);
+    }
+  } else {
+    const bool f16 = p.out_dtype == FI_DTYPE_F16;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 64) {
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = acc[C0 + c + ch * 8 + 2 * i], hi = acc[C0 + c + ch * 8 + 2 * i + 1];
+          w[i] = (uint32_t)f32_to_out(lo, f16) | ((uint32_t)f32_to_out(hi, f16) << 16);
+        }
+        put(ch, w[0], w[1], w[2], w[3]);
+      }
+      flush(col0 + c, 8);
+    }
+  }
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_wide_kernel(const WideArgs w, const __grid_constant__ CUtensorMap tmap_a,
+                    const __grid_constant__ CUtensorMap tmap_w0, const __grid_constant__ CUtensorMap tmap_w1) {
+  const Fp8MmArgs& p = w.p;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ volatile int abort_flag;
+  __shared__ uint32_t tmem_slot;
+  const uint32_t raw_s = smem_addr(smem_raw);
+  const uint32_t base = (raw_s + 1023u) & ~1023u;
+  uint8_t* const basep = smem_raw + (base - raw_s);
+  uint8_t* const staging = basep + kStages * kStageBytes;
+  float* const scales = reinterpret_cast<float*>(staging + kOutBytes);  // [slot][column half][row]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(staging + kOutBytes + kScaleBytes);
+  uint64_t* const empty = full + kStages;
+  uint64_t* const tmem_full = empty + kStages;
+  uint64_t* const tmem_empty = tmem_full + kBufs;
+  uint64_t* const scale_full = tmem_empty + kBufs;
+  uint64_t* const scale_empty = scale_full + kSlots;
+  uint64_t* const drain = scale_empty + kSlots;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int64_t my_tiles = pair < w.tiles ? (w.tiles - pair + pairs - 1) / pairs : 0;
+  const int KB = p.kblocks;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&tmem_full[i], 1);
+      mbar_init(&tmem_empty[i], 16);  // the epilogue warps of both CTAs
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&scale_full[i], 1);
+      mbar_init(&scale_empty[i], 8);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0) {
+      if (lane == 0) {
+        pdl_wait();
+        const uint32_t full0 = map_to(smem_addr(full), 0);
+        const CUtensorMap* const bmap = GATED && rank == 1 ? &tmap_w1 : &tmap_w0;
+        int64_t it = 0;
+        bool ok = true;
+        for (int64_t t = 0; t < my_tiles && ok && !p.debug_stall; ++t) {
+          int tm, tn;
+          tile_at(w, pair + t * pairs, tm, tn);
+          const int ya = (tm * 2 + rank) * kRows, yb = GATED ? tn * 128 : (tn * 2 + rank) * 128;
+          for (int i = 0; i < KB; ++i, ++it) {
+            const int st = (int)(it % kStages);
+            if (it >= kStages &&
+                !mbar_wait_bounded(&empty[st], (uint32_t)((it / kStages) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u)) {
+              ok = false;
+              break;
+            }
+            const uint32_t dst = base + (uint32_t)st * kStageBytes, bar = full0 + (uint32_t)st * 8;
+            if (rank == 0) mbar_arrive_expect_tx(&full[st], kPairBytes);
+            tma_load_pair(dst, &tmap_a, i * kFp8Block, ya, bar);
+            tma_load_pair(dst + kHalfBytes, bmap, i * kFp8Block, yb, bar);
+          }
+        }
+        if (rank == 0) {  // both CTAs' copies in flight land before either gives its memory up
+          volatile int never = 0;
+          for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+            mbar_wait_bounded(&full[i % kStages], (uint32_t)(i / kStages) & 1, &never, p.timeout_ns, p.err, 4u);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = f8_idesc(256, 256);
+        const int64_t total = my_tiles * KB;
+        bool ok = true;
+        for (int64_t it = 0; it < total; ++it) {
+          const int st = (int)(it % kStages), b = (int)(it & 1);
+          ok = mbar_wait_bounded(&full[st], (uint32_t)(it / kStages) & 1, &abort_flag, p.timeout_ns, p.err, 1u) &&
+               (it < kBufs || mbar_wait_bounded(&tmem_empty[b], (uint32_t)((it / kBufs) - 1) & 1, &abort_flag,
+                                                p.timeout_ns, p.err, 1u));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t adesc = sw128_desc(base + (uint32_t)st * kStageBytes);
+          const uint64_t bdesc = sw128_desc(base + (uint32_t)st * kStageBytes + kHalfBytes);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)  // K = 32 bytes each
+            umma_f8_pair(tmem + (uint32_t)b * 256, adesc + (uint64_t)(2 * s), bdesc + (uint64_t)(2 * s), idesc, s > 0);
+          umma_commit_pair(&empty[st]);
+          umma_commit_pair(&tmem_full[b]);
+        }
+        if (!ok) {  // the MMAs in flight end before TMEM is freed
+          volatile int never = 0;
+          umma_commit_pair(drain);
+          mbar_wait_bounded(drain, 0, &never, p.timeout_ns, p.err, 8u);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      pdl_wait();
+      constexpr int kAhead = 4;
+      float sa[kAhead][4], sw[kAhead][2];
+      // the cursor of the loads runs kAhead blocks ahead of the stores
+      int64_t lt = 0;
+      int li = 0, ltm = 0, ltn = 0;
+      if (my_tiles > 0) tile_at(w, pair, ltm, ltn);
+      const int64_t wblocks = (p.n + kFp8Block - 1) / kFp8Block;
+      auto load = [&](int d) {
+        if (lt < my_tiles) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t row = ((int64_t)ltm * 2 + rank) * kRows + lane + 32 * r;
+            sa[d][r] = row < p.m ? __ldg(p.As + row * KB + li) : 0.0f;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t blk = GATED ? ltn : (int64_t)ltn * 2 + h;
+            sw[d][h] = blk < wblocks ? __ldg(p.Ws[GATED ? h : 0] + blk * KB + li) : 0.0f;
+          }
+          if (++li == KB) {
+            li = 0;
+            if (++lt < my_tiles) tile_at(w, pair + lt * pairs, ltm, ltn);
+          }
+        }
+      };
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) load(d);
+      const int64_t total = my_tiles * KB;
+      bool ok = true;
+      for (int64_t it0 = 0; it0 < total && ok; it0 += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const int64_t it = it0 + d;
+          if (it < total && ok) {
+            const int sl = (int)(it % kSlots);
+            if (it >= kSlots)
+              ok = mbar_wait_bounded(&scale_empty[sl], (uint32_t)((it / kSlots) - 1) & 1, &abort_flag, p.timeout_ns,
+                                     p.err, 2u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              float* dst = scales + sl * (2 * kRows);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dst[h * kRows + lane + 32 * r] = sa[d][r] * sw[d][h];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&scale_full[sl]);
+              load(d);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int epi = warp - 4, quarter = warp & 3, half = epi >> 2;
+    uint8_t* const stage = staging + epi * 4096;
+    const uint32_t empty0 = map_to(smem_addr(tmem_empty), 0);
+    int64_t it = 0;
+    bool ok = true;
+    for (int64_t t = 0; t < my_tiles; ++t) {  // after a timeout: only the barriers below
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      for (int i = 0; i < KB && ok; ++i, ++it) {
+        const int b = (int)(it & 1), sl = (int)(it % kSlots);
+        ok = mbar_wait_bounded(&scale_full[sl], (uint32_t)(it / kSlots) & 1, &abort_flag, p.timeout_ns, p.err, 16u) &&
+             mbar_wait_bounded(&tmem_full[b], (uint32_t)(it / kBufs) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const float s = scales[sl * (2 * kRows) + half * kRows + quarter * 32 + lane];
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256 + half * 128);
+        uint32_t d[2][32];
+        tmem_ld32(taddr, d[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait32(d[c & 1]);
+          if (c < 3) tmem_ld32(taddr + 32 * (c + 1), d[(c + 1) & 1]);
+#pragma unroll
+          for (int q = 0; q < 32; q += 2)
+            fma_pair(acc[32 * c + q], acc[32 * c + q + 1], d[c & 1][q], d[c & 1][q + 1], s);
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_remote(empty0 + (uint32_t)b * 8);
+          mbar_arrive(&scale_empty[sl]);
+        }
+      }
+      if (GATED) {
+        // both halves of the columns meet in shared memory: each warpgroup finishes 64 of the 128
+        // (every warp passes the same number of these barriers, after a timeout too)
+        float* const gx = reinterpret_cast<float*>(staging);               // gate columns for half 1
+        float* const ux = reinterpret_cast<float*>(staging + kOutBytes / 2);  // up columns for half 0
+        const int at = quarter * 32 + lane;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          epilogue_sync();
+          if (half == 0) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) gx[c * kRows + at] = acc[64 + 32 * r + c];
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ux[c * kRows + at] = acc[32 * r + c];
+          }
+          epilogue_sync();
+          if (half == 0) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) acc[32 * r + c] = silu(acc[32 * r + c]) * ux[c * kRows + at];
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) acc[64 + 32 * r + c] = silu(gx[c * kRows + at]) * acc[64 + 32 * r + c];
+          }
+        }
+        epilogue_sync();
+      }
+      if (ok) {
+        int tm, tn;
+        tile_at(w, pair + t * pairs, tm, tn);
+        const int64_t row0 = ((int64_t)tm * 2 + rank) * kRows + quarter * 32;
+        if (!GATED)
+          store_rows<0, 128>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + half * 128);
+        else if (half == 0)
+          store_rows<0, 64>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128);
+        else
+          store_rows<64, 64>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128 + 64);
+      }
+    }
+  }
+
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other's MMAs or arrivals may reach it
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+}  // namespace
+
+int launch_fp8_wide(Fp8MmArgs a, bool gated, cudaStream_t stream) {
+  WideArgs w;
+  w.p = a;
+  const int64_t tiles_m = (a.m + 255) / 256, tiles_n = gated ? (a.n + 127) / 128 : (a.n + 255) / 256;
+  if (a.n > 0x7ffffe00LL || a.m > 0x7ffffe00LL || a.k > 0x7fffff00LL)
+    return set_error(FI_ERR_UNSUPPORTED_SHAPE, "m=%lld n=%lld k=%lld is too large", (long long)a.m, (long long)a.n,
+                     (long long)a.k);
+  w.p.tiles_m = (int)tiles_m;
+  w.p.splits = 1;
+  w.tiles_n = (int)tiles_n;
+  w.tiles = tiles_m * tiles_n;
+  w.wide_stores = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.n * (a.out_dtype == FI_DTYPE_F32 ? 4 : 2) % 16 == 0;
+  CUtensorMap ta, tw[2];
+  int rc = encode_codes(&ta, a.A, a.k, a.m, kRows);
+  for (int t = 0; t < (gated ? 2 : 1) && rc == FI_OK; ++t) rc = encode_codes(&tw[t], a.W[t], a.k, a.n, 128);
+  if (rc != FI_OK) return rc;
+  if (!gated) tw[1] = tw[0];
+  auto kern = gated ? fp8_wide_kernel<true> : fp8_wide_kernel<false>;
+  static std::atomic<int> configured[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return set_cuda_error("cudaGetDevice");
+  const int bit = gated ? 2 : 1;
+  if (!(configured[dev] & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+      return set_cuda_error("cudaFuncSetAttribute(fp8 wide smem)");
+    configured[dev] |= bit;
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(w.tiles, device_sm_count() / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, w, ta, tw[0], tw[1]) != cudaSuccess) return set_cuda_error("fp8_wide_kernel launch");
+  return FI_OK;
+}
+
+}  // namespace fi

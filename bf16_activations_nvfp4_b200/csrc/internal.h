@@ -206,6 +206,8 @@ struct Fp8MmArgs {
   uint64_t timeout_ns;   // limit of every mbarrier wait
 };
 int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream);
+// The CTA-pair kernel for many activation rows (launch_fp8_mm decides).
+int launch_fp8_wide(Fp8MmArgs a, bool gated, cudaStream_t stream);
 
 // -------------------------------------------------------------- token log probabilities
 constexpr int kLogprobMaxTopk = 32;

@@ -116,6 +116,28 @@ def test_whole_numbers_are_exact(m, n, k):
     assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all())
 
 
+@pytest.mark.parametrize("m,n,k", [(2500, 5000, 400), (3000, 2501, 128), (257, 20000, 16)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_tiles(m, n, k, dtype):
+    """More output tiles than the GPU holds at once, with ragged edges, in every type; rows around
+    the output stay as they were."""
+    a, w = _whole(m, k, 1, 1), _whole(n, k, 128, 2)
+    ref, _ = _fp8.product(a, w)
+    buf = torch.full((m + 2, n), 7.0, device="cuda", dtype=dtype)
+    fi.mm_fp8(*_fp8.cuda(a), *_fp8.cuda(w), out=buf[1:m + 1])
+    _fp8.check(buf[1:m + 1], ref, torch.zeros_like(ref))
+    assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(2500, 3000, 400), (1300, 2501, 144)])
+def test_many_gated_tiles(m, n, k):
+    a, g, u = _whole(m, k, 1, 1), _whole(n, k, 128, 2), _whole(n, k, 128, 3)
+    g = (g[0], g[1] * 2.0 ** -8)
+    (gr, gm), (ur, um) = _fp8.product(a, g), _fp8.product(a, u)
+    ref, tol = _fp8.gated(gr, 0 * gm, ur, 0 * um, k)
+    _fp8.check(fi.mm_fp8_gated(*_fp8.cuda(a), *_fp8.cuda(g), *_fp8.cuda(u)), ref, tol)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 2048), (3, 1000, 2688), (16, 640, 7168), (31, 513, 5120), (77, 1030, 2704),
                                    (200, 384, 1024), (300, 500, 1040), (1100, 900, 656), (2048, 1024, 1024)])
