@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       for (int i = 0; i < KB && !p.debug_stall; ++i) {
         const int st = i % G::kStages;
         if (i >= G::kStages &&
-            !mbar_wait_bounded(&empty[st], ((i / G::kStages) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u))
+            !mbar_wait_spin(&empty[st], ((i / G::kStages) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u))
           break;
         const uint32_t dst = base + (uint32_t)st * G::kStageBytes;
         const int x = (kb0 + i) * kFp8Block;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       // the copies in flight land before the CTA's shared memory is given up
       volatile int never = 0;
       for (int i = max(0, issued - G::kStages); i < issued; ++i)
-        mbar_wait_bounded(&full[i % G::kStages], (i / G::kStages) & 1, &never, p.timeout_ns, p.err, 4u);
+        mbar_wait_spin(&full[i % G::kStages], (i / G::kStages) & 1, &never, p.timeout_ns, p.err, 4u);
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       bool ok = true;
       for (int i = 0; i < KB; ++i) {
         const int st = i % G::kStages, b = i % G::kBufs;
-        ok = mbar_wait_bounded(&full[st], (i / G::kStages) & 1, &abort_flag, p.timeout_ns, p.err, 1u) &&
+        ok = mbar_wait_spin(&full[st], (i / G::kStages) & 1, &abort_flag, p.timeout_ns, p.err, 1u) &&
              (i < G::kBufs ||
-              mbar_wait_bounded(&tmem_empty[b], ((i / G::kBufs) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 1u));
+              mbar_wait_spin(&tmem_empty[b], ((i / G::kBufs) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 1u));
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t stage = base + (uint32_t)st * G::kStageBytes;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       if (!ok) {  // the MMAs in flight end before TMEM is freed
         volatile int never = 0;
         umma_commit(drain);
-        mbar_wait_bounded(drain, 0, &never, p.timeout_ns, p.err, 8u);
+        mbar_wait_spin(drain, 0, &never, p.timeout_ns, p.err, 8u);
       }
     }
     __syncwarp();
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
         if (i < KB && ok) {
           const int sl = i % kScaleSlots;
           if (i >= kScaleSlots)
-            ok = mbar_wait_bounded(&scale_empty[sl], ((i / kScaleSlots) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u);
+            ok = mbar_wait_spin(&scale_empty[sl], ((i / kScaleSlots) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             float* dst = scales + sl * (G::kTiles * N);
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     bool ok = true;
     for (int i = 0; i < KB; ++i) {
       const int b = i % G::kBufs, sl = i % kScaleSlots;
-      ok = mbar_wait_bounded(&scale_full[sl], (i / kScaleSlots) & 1, &abort_flag, p.timeout_ns, p.err, 16u) &&
-           mbar_wait_bounded(&tmem_full[b], (i / G::kBufs) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
+      ok = mbar_wait_spin(&scale_full[sl], (i / kScaleSlots) & 1, &abort_flag, p.timeout_ns, p.err, 16u) &&
+           mbar_wait_spin(&tmem_full[b], (i / G::kBufs) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

@@ -10,6 +10,38 @@
 
 namespace fi {
 
+// mbar_wait_bounded (sync.cuh) for waits of a few hundred cycles: no time to suspend is named, so a
+// waiting thread is back as soon as the hardware notices the phase; the clock is read now and then.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               uint64_t timeout_ns, unsigned* err_word, unsigned err_bit) {
+  const uint32_t b = smem_addr(bar);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test(b, parity)) return true;
+    if (i % 256 == 0) {  // reading the clock takes long: not in a wait that is about to end
+      if (*abort_flag) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > timeout_ns) {
+        *abort_flag = 1;
+        atomicOr(err_word, err_bit);
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(

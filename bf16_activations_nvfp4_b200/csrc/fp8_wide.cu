@@ -27,14 +27,17 @@ namespace fi {
 
 namespace {
 
-constexpr int kStages = 5, kBufs = 2, kSlots = 8, kThreads = 384;
+constexpr int kStages = 5, kBufs = 2, kThreads = 384;
+constexpr int kGroup = 8, kGroups = 2;                          // blocks of k whose scales share a barrier; groups in the ring
 constexpr int kRows = 128;                                      // activation rows of a CTA
 constexpr uint32_t kHalfBytes = kRows * 128, kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kPairBytes = 2 * kStageBytes;                // bytes a full barrier waits for
-constexpr uint32_t kOutBytes = 32 * 1024;                       // staging of the epilogue: 4 KB per warp
-constexpr uint32_t kScaleBytes = kSlots * 2 * kRows * 4;
+constexpr uint32_t kOutBytes = 16 * 1024;                       // staging of the epilogue: 2 KB per warp
+constexpr uint32_t kScaleBytes = kGroups * kGroup * 2 * kRows * 4;
+constexpr uint32_t kBarBytes = (2 * kStages + kBufs + 2 * kGroups + 1) * 8;
 constexpr int kGroupM = 8;
-constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kScaleBytes + 256;
+constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kScaleBytes + kBarBytes;
+static_assert(32 * 64 <= kOutBytes / 8, "a warp stages 64 bytes of 32 rows");
 constexpr int kEpiRegs = 216, kOtherRegs = 64;
 // registers after the split: the epilogue's two warpgroups and the other one stay within the launch's 168 a thread
 static_assert(256 * kEpiRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
@@ -107,6 +110,18 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// Keeps uses of registers that an earlier tmem_wait32 covered below it.
+__device__ __forceinline__ void tmem_pass32(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 // (x, y) += (a, b) * s, both lanes of one packed instruction.
 __device__ __forceinline__ void fma_pair(float& x, float& y, uint32_t a, uint32_t b, float s) {
   asm("{\n .reg .b64 d, e, f;\n mov.b64 d, {%2, %3};\n mov.b64 e, {%4, %4};\n mov.b64 f, {%0, %1};\n"
@@ -114,8 +129,6 @@ __device__ __forceinline__ void fma_pair(float& x, float& y, uint32_t a, uint32_
       : "+f"(x), "+f"(y)
       : "r"(a), "r"(b), "f"(s));
 }
-
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 struct WideArgs {
   Fp8MmArgs p;
@@ -134,25 +147,27 @@ __device__ __forceinline__ void tile_at(const WideArgs& w, int64_t t, int& tm, i
   tm = g * kGroupM + (r - tn * gm);
 }
 
-// One warp's 32 rows x kCols columns of `acc` (from column C0 on) to out rows row0.., columns
-// col0..: through 4 KB of shared memory, so that a row's 128 bytes leave together.
-template <int C0, int kCols>
+// One warp's 32 rows x 64 columns of `acc` (from C0 on) to out rows row0.., columns col0..: through
+// 2 KB of shared memory, so that 64 bytes of a row leave together.
+template <int C0>
 __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const float (&acc)[128], uint8_t* stage,
                                            int lane, int64_t row0, int64_t col0) {
-  const bool f32 = p.out_dtype == FI_DTYPE_F32;
-  const int es = f32 ? 4 : 2;
+  const bool f32 = p.out_dtype == FI_DTYPE_F32, f16 = p.out_dtype == FI_DTYPE_F16;
+  const int es = f32 ? 4 : 2, per = 16 / es;  // elements per 16 bytes
   const uint32_t sbase = smem_addr(stage);
   uint8_t* const out = static_cast<uint8_t*>(p.out);
-  auto flush = [&](int64_t col, int per) {  // 128 bytes of each of the 32 rows, from `col` on; `per` elements per 16 bytes
+  // 16-byte piece ch of row r; the rows' pieces are permuted so that no two lanes meet in a bank
+  auto piece = [&](int r, int ch) { return sbase + (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) * 16)); };
+  auto flush = [&](int64_t col) {
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + lane / 8, ch = lane % 8;
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + lane / 4, ch = lane % 4;
+      const int64_t row = row0 + r, c = col + ch * per;
       uint4 v;
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(sbase + (uint32_t)(r * 128 + ((ch ^ (r & 7)) * 16))));
-      const int64_t row = row0 + r, c = col + ch * per;
+                   : "r"(piece(r, ch)));
       if (row < p.m && c < p.n) {
         uint8_t* dst = out + (row * p.n + c) * es;
         if (wide && c + per <= p.n) {
@@ -174,27 +189,24 @@ __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const 
     __syncwarp();
   };
   auto put = [&](int ch, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                     sbase + (uint32_t)(lane * 128 + ((ch ^ (lane & 7)) * 16))),
-                 "r"(a), "r"(b), "r"(c), "r"(d)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(lane, ch)), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
   };
   if (f32) {
 #pragma unroll
-    for (int c = 0; c < kCols; c += 32) {
+    for (int c = 0; c < 64; c += 16) {
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
+      for (int ch = 0; ch < 4; ++ch) {
         const float* a = acc + C0 + c + ch * 4;
         put(ch, __float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
       }
-      flush(col0 + c, 4);
+      flush(col0 + c);
     }
   } else {
-    const bool f16 = p.out_dtype == FI_DTYPE_F16;
 #pragma unroll
-    for (int c = 0; c < kCols; c += 64) {
+    for (int c = 0; c < 64; c += 32) {
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
+      for (int ch = 0; ch < 4; ++ch) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -203,7 +215,7 @@ __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const 
         }
         put(ch, w[0], w[1], w[2], w[3]);
       }
-      flush(col0 + c, 8);
+      flush(col0 + c);
     }
   }
 }
@@ -220,14 +232,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw_s + 1023u) & ~1023u;
   uint8_t* const basep = smem_raw + (base - raw_s);
   uint8_t* const staging = basep + kStages * kStageBytes;
-  float* const scales = reinterpret_cast<float*>(staging + kOutBytes);  // [slot][column half][row]
+  float* const scales = reinterpret_cast<float*>(staging + kOutBytes);  // [group][block][column half][row]
   uint64_t* const full = reinterpret_cast<uint64_t*>(staging + kOutBytes + kScaleBytes);
-  uint64_t* const empty = full + kStages;
-  uint64_t* const tmem_full = empty + kStages;
-  uint64_t* const tmem_empty = tmem_full + kBufs;
+  // a block's MMAs are complete: its stage may be refilled and its sums read. One commit for both:
+  // a commit takes about 200 cycles and the next one waits for it
+  uint64_t* const done = full + kStages;
+  uint64_t* const tmem_empty = done + kStages;
   uint64_t* const scale_full = tmem_empty + kBufs;
-  uint64_t* const scale_empty = scale_full + kSlots;
-  uint64_t* const drain = scale_empty + kSlots;
+  uint64_t* const scale_empty = scale_full + kGroups;
+  uint64_t* const drain = scale_empty + kGroups;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -239,13 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&done[i], 1);
     }
     for (int i = 0; i < kBufs; ++i) {
-      mbar_init(&tmem_full[i], 1);
       mbar_init(&tmem_empty[i], 16);  // the epilogue warps of both CTAs
     }
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&scale_full[i], 1);
       mbar_init(&scale_empty[i], 8);
     }
@@ -272,16 +284,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         pdl_wait();
         const uint32_t full0 = map_to(smem_addr(full), 0);
         const CUtensorMap* const bmap = GATED && rank == 1 ? &tmap_w1 : &tmap_w0;
-        int64_t it = 0;
-        bool ok = true;
+        int st = 0;
+        uint32_t phase = 0;   // of the stage's round: the first has nothing to wait for
+        bool first = true, ok = true;
+        int64_t issued = 0;
         for (int64_t t = 0; t < my_tiles && ok && !p.debug_stall; ++t) {
           int tm, tn;
           tile_at(w, pair + t * pairs, tm, tn);
           const int ya = (tm * 2 + rank) * kRows, yb = GATED ? tn * 128 : (tn * 2 + rank) * 128;
-          for (int i = 0; i < KB; ++i, ++it) {
-            const int st = (int)(it % kStages);
-            if (it >= kStages &&
-                !mbar_wait_bounded(&empty[st], (uint32_t)((it / kStages) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u)) {
+          for (int i = 0; i < KB; ++i) {
+            if (!first &&
+                !mbar_wait_spin(&done[st], phase ^ 1, &abort_flag, p.timeout_ns, p.err, 2u)) {
               ok = false;
               break;
             }
@@ -289,12 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(&full[st], kPairBytes);
             tma_load_pair(dst, &tmap_a, i * kFp8Block, ya, bar);
             tma_load_pair(dst + kHalfBytes, bmap, i * kFp8Block, yb, bar);
+            ++issued;
+            if (++st == kStages) {
+              st = 0;
+              phase ^= 1;
+              first = false;
+            }
           }
         }
         if (rank == 0) {  // both CTAs' copies in flight land before either gives its memory up
           volatile int never = 0;
-          for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-            mbar_wait_bounded(&full[i % kStages], (uint32_t)(i / kStages) & 1, &never, p.timeout_ns, p.err, 4u);
+          for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            mbar_wait_spin(&full[i % kStages], (uint32_t)(i / kStages) & 1, &never, p.timeout_ns, p.err, 4u);
         }
       }
       __syncwarp();
@@ -302,26 +321,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && rank == 0) {
         constexpr uint32_t idesc = f8_idesc(256, 256);
         const int64_t total = my_tiles * KB;
+        int st = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int64_t it = 0; it < total; ++it) {
-          const int st = (int)(it % kStages), b = (int)(it & 1);
-          ok = mbar_wait_bounded(&full[st], (uint32_t)(it / kStages) & 1, &abort_flag, p.timeout_ns, p.err, 1u) &&
-               (it < kBufs || mbar_wait_bounded(&tmem_empty[b], (uint32_t)((it / kBufs) - 1) & 1, &abort_flag,
-                                                p.timeout_ns, p.err, 1u));
+          const uint32_t b = (uint32_t)it & 1;
+          ok = mbar_wait_spin(&full[st], phase, &abort_flag, p.timeout_ns, p.err, 1u) &&
+               (it < kBufs || mbar_wait_spin(&tmem_empty[b], ((uint32_t)it / kBufs - 1) & 1, &abort_flag,
+                                             p.timeout_ns, p.err, 1u));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint64_t adesc = sw128_desc(base + (uint32_t)st * kStageBytes);
           const uint64_t bdesc = sw128_desc(base + (uint32_t)st * kStageBytes + kHalfBytes);
 #pragma unroll
           for (int s = 0; s < 4; ++s)  // K = 32 bytes each
-            umma_f8_pair(tmem + (uint32_t)b * 256, adesc + (uint64_t)(2 * s), bdesc + (uint64_t)(2 * s), idesc, s > 0);
-          umma_commit_pair(&empty[st]);
-          umma_commit_pair(&tmem_full[b]);
+            umma_f8_pair(tmem + b * 256, adesc + (uint64_t)(2 * s), bdesc + (uint64_t)(2 * s), idesc, s > 0);
+          umma_commit_pair(&done[st]);
+          if (++st == kStages) {
+            st = 0;
+            phase ^= 1;
+          }
         }
         if (!ok) {  // the MMAs in flight end before TMEM is freed
           volatile int never = 0;
           umma_commit_pair(drain);
-          mbar_wait_bounded(drain, 0, &never, p.timeout_ns, p.err, 8u);
+          mbar_wait_spin(drain, 0, &never, p.timeout_ns, p.err, 8u);
         }
       }
       __syncwarp();
@@ -355,105 +379,106 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int d = 0; d < kAhead; ++d) load(d);
       const int64_t total = my_tiles * KB;
+      uint32_t g = 0, phase = 1;  // the first round of groups is free
       bool ok = true;
-      for (int64_t it0 = 0; it0 < total && ok; it0 += kAhead) {
+      static_assert(kGroup % kAhead == 0, "a group is whole batches of loads");
+      for (int64_t it0 = 0; it0 < total && ok; it0 += kGroup) {
+        if (it0 >= kGroups * kGroup)
+          ok = mbar_wait_spin(&scale_empty[g], phase, &abort_flag, p.timeout_ns, p.err, 2u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        float* dst = scales + g * (kGroup * 2 * kRows);
+#pragma unroll 1
+        for (int j = 0; j < kGroup; j += kAhead) {
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-          const int64_t it = it0 + d;
-          if (it < total && ok) {
-            const int sl = (int)(it % kSlots);
-            if (it >= kSlots)
-              ok = mbar_wait_bounded(&scale_empty[sl], (uint32_t)((it / kSlots) - 1) & 1, &abort_flag, p.timeout_ns,
-                                     p.err, 2u);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
-              float* dst = scales + sl * (2 * kRows);
+          for (int d = 0; d < kAhead; ++d) {
+            if (it0 + j + d < total) {
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dst[h * kRows + lane + 32 * r] = sa[d][r] * sw[d][h];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&scale_full[sl]);
+                for (int r = 0; r < 4; ++r) dst[(j + d) * 2 * kRows + h * kRows + lane + 32 * r] = sa[d][r] * sw[d][h];
               load(d);
             }
           }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scale_full[g]);
+        if (++g == kGroups) {
+          g = 0;
+          phase ^= 1;
         }
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int epi = warp - 4, quarter = warp & 3, half = epi >> 2;
-    uint8_t* const stage = staging + epi * 4096;
+    uint8_t* const stage = staging + epi * (kOutBytes / 8);
     const uint32_t empty0 = map_to(smem_addr(tmem_empty), 0);
     int64_t it = 0;
+    int st = 0;
+    uint32_t phase = 0;
     bool ok = true;
-    for (int64_t t = 0; t < my_tiles; ++t) {  // after a timeout: only the barriers below
+    for (int64_t t = 0; t < my_tiles && ok; ++t) {
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
-      for (int i = 0; i < KB && ok; ++i, ++it) {
-        const int b = (int)(it & 1), sl = (int)(it % kSlots);
-        ok = mbar_wait_bounded(&scale_full[sl], (uint32_t)(it / kSlots) & 1, &abort_flag, p.timeout_ns, p.err, 16u) &&
-             mbar_wait_bounded(&tmem_full[b], (uint32_t)(it / kBufs) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
+      for (int i = 0; i < KB; ++i) {
+        const uint32_t it32 = (uint32_t)it, b = it32 & 1, g = it32 / kGroup % kGroups;
+        if (it32 % kGroup == 0)
+          ok = mbar_wait_spin(&scale_full[g], it32 / (kGroup * kGroups) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
+        ok = ok && mbar_wait_spin(&done[st], phase, &abort_flag, p.timeout_ns, p.err, 16u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const float s = scales[sl * (2 * kRows) + half * kRows + quarter * 32 + lane];
-        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256 + half * 128);
-        uint32_t d[2][32];
-        tmem_ld32(taddr, d[0]);
+        const float* const sp = scales + (it32 % (kGroup * kGroups)) * (2 * kRows) + quarter * 32 + lane;
+        const float s[2] = {sp[0], sp[kRows]};
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + b * 256 + (uint32_t)(half * 64);
+        // 64 columns at a time in two loads: the buffer is held for two load latencies
+        uint32_t d0[32], d1[32];
+        tmem_ld32(taddr, d0);
+        tmem_ld32(taddr + 32, d1);
+        tmem_wait32(d0);
+        tmem_pass32(d1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait32(d[c & 1]);
-          if (c < 3) tmem_ld32(taddr + 32 * (c + 1), d[(c + 1) & 1]);
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[q], acc[q + 1], d0[q], d0[q + 1], s[0]);
+        tmem_ld32(taddr + 128, d0);
 #pragma unroll
-          for (int q = 0; q < 32; q += 2)
-            fma_pair(acc[32 * c + q], acc[32 * c + q + 1], d[c & 1][q], d[c & 1][q + 1], s);
-        }
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[32 + q], acc[33 + q], d1[q], d1[q + 1], s[0]);
+        tmem_ld32(taddr + 160, d1);
+        tmem_wait32(d0);
+        tmem_pass32(d1);
+        // everything is in registers: the buffer and the slot are free
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_remote(empty0 + (uint32_t)b * 8);
-          mbar_arrive(&scale_empty[sl]);
+          if (rank == 0)
+            mbar_arrive(&tmem_empty[b]);
+          else
+            mbar_arrive_remote(empty0 + b * 8);
+          if (it32 % kGroup == kGroup - 1) mbar_arrive(&scale_empty[g]);
         }
-      }
-      if (GATED) {
-        // both halves of the columns meet in shared memory: each warpgroup finishes 64 of the 128
-        // (every warp passes the same number of these barriers, after a timeout too)
-        float* const gx = reinterpret_cast<float*>(staging);               // gate columns for half 1
-        float* const ux = reinterpret_cast<float*>(staging + kOutBytes / 2);  // up columns for half 0
-        const int at = quarter * 32 + lane;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          epilogue_sync();
-          if (half == 0) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) gx[c * kRows + at] = acc[64 + 32 * r + c];
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) ux[c * kRows + at] = acc[32 * r + c];
-          }
-          epilogue_sync();
-          if (half == 0) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) acc[32 * r + c] = silu(acc[32 * r + c]) * ux[c * kRows + at];
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) acc[64 + 32 * r + c] = silu(gx[c * kRows + at]) * acc[64 + 32 * r + c];
-          }
+        ++it;
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
         }
-        epilogue_sync();
+#pragma unroll
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[64 + q], acc[65 + q], d0[q], d0[q + 1], s[1]);
+#pragma unroll
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[96 + q], acc[97 + q], d1[q], d1[q + 1], s[1]);
       }
       if (ok) {
         int tm, tn;
         tile_at(w, pair + t * pairs, tm, tn);
         const int64_t row0 = ((int64_t)tm * 2 + rank) * kRows + quarter * 32;
-        if (!GATED)
-          store_rows<0, 128>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + half * 128);
-        else if (half == 0)
-          store_rows<0, 64>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128);
-        else
-          store_rows<64, 64>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128 + 64);
+        if (GATED) {  // the first 64 columns are gates, the others their up columns
+#pragma unroll
+          for (int c = 0; c < 64; ++c) acc[c] = silu(acc[c]) * acc[64 + c];
+          store_rows<0>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128 + half * 64);
+        } else {
+          store_rows<0>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + half * 64);
+          store_rows<64>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + 128 + half * 64);
+        }
       }
     }
   }
