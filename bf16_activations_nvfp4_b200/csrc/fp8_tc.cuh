@@ -22,9 +22,8 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ bool mbar_wait_addr(uint32_t b, uint32_t parity, volatile int* abort_flag,
                                                uint64_t timeout_ns, unsigned* err_word, unsigned err_bit) {
-  const uint32_t b = smem_addr(bar);
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
@@ -40,6 +39,11 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, v
       }
     }
   }
+}
+
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               uint64_t timeout_ns, unsigned* err_word, unsigned err_bit) {
+  return mbar_wait_addr(smem_addr(bar), parity, abort_flag, timeout_ns, err_word, err_bit);
 }
 
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,

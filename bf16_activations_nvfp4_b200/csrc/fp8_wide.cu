@@ -8,7 +8,7 @@
 //   warp 0      TMA producer of its 128 A rows and 128 B rows, a ring of 5 stages; the bytes of
 //               both CTAs complete one barrier, in the pair's first CTA;
 //   warp 1      in the first CTA, one thread issues the MMAs for both; the commits arrive in both;
-//   warp 2      the scales As * Ws of a block, several blocks ahead, into a small ring;
+//   warps 2-3   the scales As * Ws of a block, up to 16 blocks ahead, into a ring;
 //   warps 4-11  epilogue, one thread per activation row and half of the columns (128): a block's
 //               sums, times the row's scale, are added to 128 fp32 registers while the tensor
 //               cores fill the other TMEM buffer. setmaxnreg gives these warps 216 registers.
@@ -32,12 +32,12 @@ constexpr int kGroup = 8, kGroups = 2;                          // blocks of k w
 constexpr int kRows = 128;                                      // activation rows of a CTA
 constexpr uint32_t kHalfBytes = kRows * 128, kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kPairBytes = 2 * kStageBytes;                // bytes a full barrier waits for
-constexpr uint32_t kOutBytes = 16 * 1024;                       // staging of the epilogue: 2 KB per warp
+constexpr uint32_t kOutBytes = 32 * 1024;                       // staging of the epilogue: 4 KB per warp
 constexpr uint32_t kScaleBytes = kGroups * kGroup * 2 * kRows * 4;
 constexpr uint32_t kBarBytes = (2 * kStages + kBufs + 2 * kGroups + 1) * 8;
 constexpr int kGroupM = 8;
 constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kScaleBytes + kBarBytes;
-static_assert(32 * 64 <= kOutBytes / 8, "a warp stages 64 bytes of 32 rows");
+static_assert(32 * 128 <= kOutBytes / 8, "a warp stages 128 bytes of 32 rows");
 constexpr int kEpiRegs = 216, kOtherRegs = 64;
 // registers after the split: the epilogue's two warpgroups and the other one stay within the launch's 168 a thread
 static_assert(256 * kEpiRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
@@ -84,8 +84,11 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 // Arrives on a barrier of the pair. It orders TMEM reads only (a tcgen05 fence precedes it), so the
 // default scope is enough: with cluster scope each arrival is a memory barrier, and the kernel ran
 // at half its speed.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+__device__ __forceinline__ void mbar_arrive_remote_if(uint32_t yes, uint32_t addr) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %0, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%1];\n}" ::"r"(yes),
+      "r"(addr)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -148,43 +151,42 @@ __device__ __forceinline__ void tile_at(const WideArgs& w, int64_t t, int& tm, i
 }
 
 // One warp's 32 rows x 64 columns of `acc` (from C0 on) to out rows row0.., columns col0..: through
-// 2 KB of shared memory, so that 64 bytes of a row leave together.
+// 4 KB of shared memory, so that 128 bytes of a row leave together.
 template <int C0>
 __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const float (&acc)[128], uint8_t* stage,
                                            int lane, int64_t row0, int64_t col0) {
   const bool f32 = p.out_dtype == FI_DTYPE_F32, f16 = p.out_dtype == FI_DTYPE_F16;
   const int es = f32 ? 4 : 2, per = 16 / es;  // elements per 16 bytes
   const uint32_t sbase = smem_addr(stage);
-  uint8_t* const out = static_cast<uint8_t*>(p.out);
+  const int64_t pitch = p.n * es;
   // 16-byte piece ch of row r; the rows' pieces are permuted so that no two lanes meet in a bank
-  auto piece = [&](int r, int ch) { return sbase + (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) * 16)); };
+  auto piece = [&](int r, int ch) { return sbase + (uint32_t)(r * 128 + ((ch ^ (r & 7)) * 16)); };
   auto flush = [&](int64_t col) {
     __syncwarp();
+    const int r = lane / 8, ch = lane % 8;
+    uint8_t* dst = static_cast<uint8_t*>(p.out) + (row0 + r) * pitch + (col + ch * per) * es;
+    const bool whole = wide && row0 + 32 <= p.m && col + 8 * per <= p.n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + lane / 4, ch = lane % 4;
-      const int64_t row = row0 + r, c = col + ch * per;
+    for (int i = 0; i < 8; ++i) {
       uint4 v;
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(piece(r, ch)));
-      if (row < p.m && c < p.n) {
-        uint8_t* dst = out + (row * p.n + c) * es;
-        if (wide && c + per <= p.n) {
-          *reinterpret_cast<uint4*>(dst) = v;
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                   : "r"(piece(i * 4 + r, ch)));
+      if (whole) {
+        *reinterpret_cast<uint4*>(dst) = v;
+      } else if (row0 + i * 4 + r < p.m) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (e < per && c + e < p.n) {
-              if (f32)
-                reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
-              else
-                reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-            }
+        for (int e = 0; e < 8; ++e) {
+          if (e < per && col + ch * per + e < p.n) {
+            if (f32)
+              reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
+            else
+              reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
           }
         }
       }
+      dst += 4 * pitch;
     }
     __syncwarp();
   };
@@ -194,9 +196,9 @@ __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const 
   };
   if (f32) {
 #pragma unroll
-    for (int c = 0; c < 64; c += 16) {
+    for (int c = 0; c < 64; c += 32) {
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
+      for (int ch = 0; ch < 8; ++ch) {
         const float* a = acc + C0 + c + ch * 4;
         put(ch, __float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
       }
@@ -204,19 +206,19 @@ __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const 
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < 64; c += 32) {
+    for (int ch = 0; ch < 8; ++ch) {
+      uint32_t w[4];
+      const float* a = acc + C0 + ch * 8;
+      if (f16) {
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t w[4];
+        for (int i = 0; i < 4; ++i) w[i] = f32x2_to_f16x2(a[2 * i], a[2 * i + 1]);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = acc[C0 + c + ch * 8 + 2 * i], hi = acc[C0 + c + ch * 8 + 2 * i + 1];
-          w[i] = (uint32_t)f32_to_out(lo, f16) | ((uint32_t)f32_to_out(hi, f16) << 16);
-        }
-        put(ch, w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; ++i) w[i] = f32x2_to_bf16x2(a[2 * i], a[2 * i + 1]);
       }
-      flush(col0 + c);
+      put(ch, w[0], w[1], w[2], w[3]);
     }
+    flush(col0);
   }
 }
 
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw_s + 1023u) & ~1023u;
   uint8_t* const basep = smem_raw + (base - raw_s);
   uint8_t* const staging = basep + kStages * kStageBytes;
-  float* const scales = reinterpret_cast<float*>(staging + kOutBytes);  // [group][block][column half][row]
+  float* const scales = reinterpret_cast<float*>(staging + kOutBytes);  // [group][block][row][column half]
   uint64_t* const full = reinterpret_cast<uint64_t*>(staging + kOutBytes + kScaleBytes);
   // a block's MMAs are complete: its stage may be refilled and its sums read. One commit for both:
   // a commit takes about 200 cycles and the next one waits for it
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tmem_empty[i], 16);  // the epilogue warps of both CTAs
     }
     for (int i = 0; i < kGroups; ++i) {
-      mbar_init(&scale_full[i], 1);
+      mbar_init(&scale_full[i], 2);
       mbar_init(&scale_empty[i], 8);
     }
     mbar_init(drain, 1);
@@ -349,63 +351,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 2) {
+    } else {
+      // warps 2 and 3: 64 rows each, two per lane; four blocks are loaded while the four before
+      // them are multiplied and stored
       pdl_wait();
-      constexpr int kAhead = 4;
-      float sa[kAhead][4], sw[kAhead][2];
-      // the cursor of the loads runs kAhead blocks ahead of the stores
-      int64_t lt = 0;
-      int li = 0, ltm = 0, ltn = 0;
-      if (my_tiles > 0) tile_at(w, pair, ltm, ltn);
+      constexpr int kBatch = 4;
+      const int r0 = (warp - 2) * 64 + lane;
       const int64_t wblocks = (p.n + kFp8Block - 1) / kFp8Block;
-      auto load = [&](int d) {
-        if (lt < my_tiles) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int64_t row = ((int64_t)ltm * 2 + rank) * kRows + lane + 32 * r;
-            sa[d][r] = row < p.m ? __ldg(p.As + row * KB + li) : 0.0f;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t blk = GATED ? ltn : (int64_t)ltn * 2 + h;
-            sw[d][h] = blk < wblocks ? __ldg(p.Ws[GATED ? h : 0] + blk * KB + li) : 0.0f;
-          }
-          if (++li == KB) {
-            li = 0;
-            if (++lt < my_tiles) tile_at(w, pair + lt * pairs, ltm, ltn);
-          }
-        }
-      };
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) load(d);
-      const int64_t total = my_tiles * KB;
-      uint32_t g = 0, phase = 1;  // the first round of groups is free
+      float* const dst0 = scales + r0 * 2;
+      float next[kBatch][4];
+      uint32_t it = 0, g = 0, phase = 1;  // blocks so far, the group, its barrier's phase
       bool ok = true;
-      static_assert(kGroup % kAhead == 0, "a group is whole batches of loads");
-      for (int64_t it0 = 0; it0 < total && ok; it0 += kGroup) {
-        if (it0 >= kGroups * kGroup)
-          ok = mbar_wait_spin(&scale_empty[g], phase, &abort_flag, p.timeout_ns, p.err, 2u);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        float* dst = scales + g * (kGroup * 2 * kRows);
-#pragma unroll 1
-        for (int j = 0; j < kGroup; j += kAhead) {
+      for (int64_t t = 0; t < my_tiles && ok; ++t) {
+        int tm, tn;
+        tile_at(w, pair + t * pairs, tm, tn);
+        const int64_t row = ((int64_t)tm * 2 + rank) * kRows + r0;
+        const int64_t blk = GATED ? tn : (int64_t)tn * 2;
+        const bool in0 = row < p.m, in1 = row + 32 < p.m, win1 = GATED || blk + 1 < wblocks;
+        const float* const a0 = p.As + (in0 ? row : 0) * KB;
+        const float* const a1 = p.As + (in1 ? row + 32 : 0) * KB;
+        const float* const w0 = p.Ws[0] + blk * KB;
+        const float* const w1 = GATED ? p.Ws[1] + blk * KB : p.Ws[0] + (win1 ? blk + 1 : 0) * KB;
+        auto load = [&](int i0) {
 #pragma unroll
-          for (int d = 0; d < kAhead; ++d) {
-            if (it0 + j + d < total) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dst[(j + d) * 2 * kRows + h * kRows + lane + 32 * r] = sa[d][r] * sw[d][h];
-              load(d);
+          for (int d = 0; d < kBatch; ++d) {
+            if (i0 + d < KB) {
+              next[d][0] = __ldg(a0 + i0 + d);
+              next[d][1] = __ldg(a1 + i0 + d);
+              next[d][2] = __ldg(w0 + i0 + d);
+              next[d][3] = __ldg(w1 + i0 + d);
             }
           }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&scale_full[g]);
-        if (++g == kGroups) {
-          g = 0;
-          phase ^= 1;
+        };
+        load(0);
+        for (int i0 = 0; i0 < KB && ok; i0 += kBatch) {
+          float v[kBatch][4];
+#pragma unroll
+          for (int d = 0; d < kBatch; ++d) {
+            v[d][0] = in0 ? next[d][0] : 0.0f;
+            v[d][1] = in1 ? next[d][1] : 0.0f;
+            v[d][2] = next[d][2];
+            v[d][3] = win1 ? next[d][3] : 0.0f;
+          }
+          load(i0 + kBatch);
+#pragma unroll
+          for (int d = 0; d < kBatch; ++d) {
+            if (i0 + d < KB && ok) {
+              if (it % kGroup == 0 && it >= kGroup * kGroups) {
+                ok = mbar_wait_spin(&scale_empty[g], phase, &abort_flag, p.timeout_ns, p.err, 2u);
+                ok = __all_sync(0xffffffffu, ok);
+              }
+              float2* const dst = reinterpret_cast<float2*>(dst0 + it % (kGroup * kGroups) * (2 * kRows));
+              dst[0] = make_float2(v[d][0] * v[d][2], v[d][0] * v[d][3]);
+              dst[32] = make_float2(v[d][1] * v[d][2], v[d][1] * v[d][3]);
+              if (++it % kGroup == 0 || (t + 1 == my_tiles && i0 + d + 1 == KB)) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&scale_full[g]);
+                if (++g == kGroups) {
+                  g = 0;
+                  phase ^= 1;
+                }
+              }
+            }
+          }
         }
       }
     }
@@ -414,25 +422,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int epi = warp - 4, quarter = warp & 3, half = epi >> 2;
     uint8_t* const stage = staging + epi * (kOutBytes / 8);
     const uint32_t empty0 = map_to(smem_addr(tmem_empty), 0);
-    int64_t it = 0;
-    int st = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int64_t t = 0; t < my_tiles && ok; ++t) {
+    // A wait that runs out raises the abort flag; the ones after it then give up quickly, and the
+    // blocks' sums are what TMEM held. So the loop below needs no way out.
+    const uint32_t done0 = smem_addr(done), done_end = done0 + kStages * 8;
+    const uint32_t sp0 = smem_addr(scales) + (uint32_t)(quarter * 32 + lane) * 8;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 64);
+    const uint32_t first = lane == 0;
+    uint32_t done_bar = done0, phase = 0;  // the next block's barrier and its phase
+    uint32_t it = 0;                       // blocks so far (its low bits count)
+    float s0, s1;                          // the scales of the next block
+    auto load_scales = [&](uint32_t i) {
+      if (i % kGroup == 0)
+        mbar_wait_spin(&scale_full[i / kGroup % kGroups], i / (kGroup * kGroups) & 1, &abort_flag, p.timeout_ns, p.err,
+                       16u);
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(s0), "=f"(s1)
+                   : "r"(sp0 + i % (kGroup * kGroups) * (2 * kRows * 4)));
+    };
+    for (int64_t t = 0; t < my_tiles; ++t) {
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      load_scales(it);
+      uint32_t ready = 0;
+#pragma unroll 1
       for (int i = 0; i < KB; ++i) {
-        const uint32_t it32 = (uint32_t)it, b = it32 & 1, g = it32 / kGroup % kGroups;
-        if (it32 % kGroup == 0)
-          ok = mbar_wait_spin(&scale_full[g], it32 / (kGroup * kGroups) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
-        ok = ok && mbar_wait_spin(&done[st], phase, &abort_flag, p.timeout_ns, p.err, 16u);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!ready) mbar_wait_addr(done_bar, phase, &abort_flag, p.timeout_ns, p.err, 16u);
+        __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const float* const sp = scales + (it32 % (kGroup * kGroups)) * (2 * kRows) + quarter * 32 + lane;
-        const float s[2] = {sp[0], sp[kRows]};
-        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + b * 256 + (uint32_t)(half * 64);
+        done_bar += 8;
+        if (done_bar == done_end) {
+          done_bar = done0;
+          phase ^= 1;
+        }
+        const uint32_t b = it & 1, taddr = lanes + b * 256;
+        const float c0 = s0, c1 = s1;
         // 64 columns at a time in two loads: the buffer is held for two load latencies
         uint32_t d0[32], d1[32];
         tmem_ld32(taddr, d0);
@@ -440,34 +464,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait32(d0);
         tmem_pass32(d1);
 #pragma unroll
-        for (int q = 0; q < 32; q += 2) fma_pair(acc[q], acc[q + 1], d0[q], d0[q + 1], s[0]);
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[q], acc[q + 1], d0[q], d0[q + 1], c0);
         tmem_ld32(taddr + 128, d0);
 #pragma unroll
-        for (int q = 0; q < 32; q += 2) fma_pair(acc[32 + q], acc[33 + q], d1[q], d1[q + 1], s[0]);
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[32 + q], acc[33 + q], d1[q], d1[q + 1], c0);
         tmem_ld32(taddr + 160, d1);
         tmem_wait32(d0);
         tmem_pass32(d1);
-        // everything is in registers: the buffer and the slot are free
+        // everything is in registers: the buffer, and at a group's end its scales, are free
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          if (rank == 0)
-            mbar_arrive(&tmem_empty[b]);
-          else
-            mbar_arrive_remote(empty0 + b * 8);
-          if (it32 % kGroup == kGroup - 1) mbar_arrive(&scale_empty[g]);
-        }
+        mbar_arrive_remote_if(first, empty0 + b * 8);
+        // the next block's barrier and scales are looked at while this one's columns are added
+        ready = mbar_test(done_bar, phase);
+        if (i + 1 < KB) load_scales(it + 1);
+        if (it % kGroup == kGroup - 1 && first) mbar_arrive(&scale_empty[it / kGroup % kGroups]);
         ++it;
-        if (++st == kStages) {
-          st = 0;
-          phase ^= 1;
-        }
 #pragma unroll
-        for (int q = 0; q < 32; q += 2) fma_pair(acc[64 + q], acc[65 + q], d0[q], d0[q + 1], s[1]);
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[64 + q], acc[65 + q], d0[q], d0[q + 1], c1);
 #pragma unroll
-        for (int q = 0; q < 32; q += 2) fma_pair(acc[96 + q], acc[97 + q], d1[q], d1[q + 1], s[1]);
+        for (int q = 0; q < 32; q += 2) fma_pair(acc[96 + q], acc[97 + q], d1[q], d1[q + 1], c1);
       }
-      if (ok) {
+      if (!abort_flag) {
         int tm, tn;
         tile_at(w, pair + t * pairs, tm, tn);
         const int64_t row0 = ((int64_t)tm * 2 + rank) * kRows + quarter * 32;
