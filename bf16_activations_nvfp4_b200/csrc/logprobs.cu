@@ -31,10 +31,10 @@ namespace fi {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBuffer = 32 + 256;  // keys a warp may hold before it merges: 31, and one vector of every lane
+constexpr int kBuffer = 64;  // keys a warp may hold before it merges: 31, and one of every lane
+constexpr int kShort = 64, kMany = 256, kFew = 1024;  // threads of a CTA: many short rows, many rows, few rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kFloor = -1e38f;  // stands for -inf: (kFloor - M) log2 e is finite, its exponential 0
+constexpr float kFloor = -0x1.2cp126f;  // stands for -inf (0xFE96 in bf16): (kFloor - M) log2 e is finite, its exponential 0
 constexpr float kFar = -1e30f;    // least difference of two maxima: times a sum it stays finite
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -66,33 +66,138 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
   return (uint64_t)order_of(x) << 32 | (uint32_t)~index;
 }
 
+// The value just below x (x finite or +inf); NaN for -inf, which has none, and for NaN.
+__device__ __forceinline__ float below(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  if (!(x > __uint_as_float(0xFF800000u))) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(b == 0 ? 0x80000001u : (b & 0x80000000u ? b + 1 : b - 1));
+}
+
+// The same of 16-bit floating-point bits, `lowest` those of -inf.
+__device__ __forceinline__ uint32_t below16(uint32_t b, uint32_t lowest) {
+  b = b == 0x8000u ? 0u : b;
+  if (b == lowest || (b & 0x7FFFu) > (lowest & 0x7FFFu)) return 0x7FFFu;  // a NaN
+  return b == 0 ? 0x8001u : (b & 0x8000u ? b + 1 : b - 1);
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// kN elements in four 32-bit words. raw: one element and masked ones in a word; wmax: the greater of two words, element by element; lift: the
+// word with its -inf replaced by a value whose exponential is 0 (for f16, once it is fp32);
+// count: n += the word's elements above those of `limit` (NaN is above everything).
 template <int DT>
 struct Elem;
 template <>
 struct Elem<FI_DTYPE_F32> {
   using T = float;
+  static constexpr uint32_t kMasked = 0xFF800000u;  // -inf in every element
   static constexpr int kN = 4;
   __device__ static float get(const uint32_t (&w)[4], int i) { return __uint_as_float(w[i]); }
   __device__ static float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+  __device__ static uint32_t raw(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
+  __device__ static uint32_t wmax(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
+  __device__ static float top(uint32_t w) { return __uint_as_float(w); }
+  __device__ static uint32_t lift(uint32_t w) { return wmax(w, __float_as_uint(kFloor)); }
+  __device__ static uint32_t spread(float x) { return __float_as_uint(x); }
+  __device__ static uint32_t before(float x) { return __float_as_uint(below(x)); }
+  __device__ static void count(uint32_t& n, uint32_t w, uint32_t limit) {
+    n += !(__uint_as_float(w) <= __uint_as_float(limit)) ? 1 : 0;
+  }
+  __device__ static uint32_t counted(uint32_t n) { return n; }
 };
 template <>
 struct Elem<FI_DTYPE_BF16> {
   using T = uint16_t;
+  static constexpr uint32_t kMasked = 0xFF80FF80u;  // -inf in every element
   static constexpr int kN = 8;
   __device__ static float get(const uint32_t (&w)[4], int i) {
     return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
   }
   __device__ static float one(const void* p, int64_t i) { return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]); }
+  __device__ static uint32_t raw(const void* p, int64_t i) {
+    return (kMasked & 0xFFFF0000u) | static_cast<const uint16_t*>(p)[i];
+  }
+  __device__ static uint32_t wmax(uint32_t a, uint32_t b) { return max_bf16x2(a, b); }
+  __device__ static float top(uint32_t w) {
+    return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  // kFloor in bf16
+  __device__ static uint32_t lift(uint32_t w) { return max_bf16x2(w, 0xFE96FE96u); }
+  __device__ static uint32_t spread(float x) { return f32x2_to_bf16x2(x, x); }
+  __device__ static uint32_t before(float x) {
+    const uint32_t b = below16((uint16_t)f32_to_bf16_rn(x), 0xFF80u);
+    return b | b << 16;
+  }
+  // greater or NaN: 1.0 each, added in bf16 (exact up to 256)
+  __device__ static void count(uint32_t& n, uint32_t w, uint32_t limit) {
+    asm("{\n .reg .b32 g;\n set.gtu.bf16x2.bf16x2 g, %1, %2;\n add.rn.bf16x2 %0, %0, g;\n}" : "+r"(n) : "r"(w), "r"(limit));
+  }
+  __device__ static uint32_t counted(uint32_t n) {
+    return (uint32_t)(__uint_as_float(n << 16) + __uint_as_float(n & 0xFFFF0000u));
+  }
 };
 template <>
 struct Elem<FI_DTYPE_F16> {
   using T = uint16_t;
+  static constexpr uint32_t kMasked = 0xFC00FC00u;  // -inf in every element
   static constexpr int kN = 8;
   __device__ static float get(const uint32_t (&w)[4], int i) {
     return i & 1 ? f16_hi_to_f32(w[i / 2]) : f16_lo_to_f32(w[i / 2]);
   }
   __device__ static float one(const void* p, int64_t i) { return f16_lo_to_f32(static_cast<const uint16_t*>(p)[i]); }
+  __device__ static uint32_t raw(const void* p, int64_t i) {
+    return (kMasked & 0xFFFF0000u) | static_cast<const uint16_t*>(p)[i];
+  }
+  __device__ static uint32_t wmax(uint32_t a, uint32_t b) { return max_f16x2(a, b); }
+  __device__ static float top(uint32_t w) { return max_nan(f16_lo_to_f32(w), f16_hi_to_f32(w)); }
+  __device__ static uint32_t lift(uint32_t w) { return w; }
+  __device__ static uint32_t spread(float x) { return f32x2_to_f16x2(x, x); }
+  __device__ static uint32_t before(float x) {
+    const uint32_t b = below16((uint16_t)f32_to_f16_rn(x), 0xFC00u);
+    return b | b << 16;
+  }
+  __device__ static void count(uint32_t& n, uint32_t w, uint32_t limit) {
+    asm("{\n .reg .b32 g;\n set.gtu.f16x2.f16x2 g, %1, %2;\n add.rn.f16x2 %0, %0, g;\n}" : "+r"(n) : "r"(w), "r"(limit));
+  }
+  __device__ static uint32_t counted(uint32_t n) { return (uint32_t)(f16_lo_to_f32(n) + f16_hi_to_f32(n)); }
 };
+
+// Packed pairs of fp32: one instruction for two elements.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 
 struct Sums {
   float m, s, t;  // maximum, sum of 2^((z - m) log2 e), sum of (z - m) times that
@@ -108,28 +213,29 @@ __device__ __forceinline__ Sums join(const Sums a, const Sums b) {
   return r;
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
-
-// The warp's 32 keys, one per lane, into ascending order by lane.
-__device__ __forceinline__ uint64_t sort32(uint64_t v, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
+// The warp's 32 keys, one per lane, into ascending order by lane. (The loops stay loops: the
+// kernel's time goes up with its code, as the instruction caches are small.)
+template <typename T>
+__device__ __forceinline__ T sort32(T v, int lane) {
+#pragma unroll 1
+  for (int size = 2; size <= 32; size *= 2) {
+    const bool up = (lane & size) == 0 || size == 32;
+#pragma unroll 1
     for (int o = size / 2; o > 0; o /= 2) {
-      const uint64_t w = shfl_xor64(v, o);
-      const bool up = (lane & size) == 0 || size == 32;
-      const bool low = (lane & o) == 0;
-      v = (low == up) == (v < w) ? v : w;
+      const T w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = (((lane & o) == 0) == up) == (v < w) ? v : w;
     }
+  }
   return v;
 }
 
 // The 32 greatest of a descending list and an ascending one, descending.
-__device__ __forceinline__ uint64_t merge32(uint64_t list, uint64_t asc, int lane) {
-  uint64_t v = list > asc ? list : asc;
-#pragma unroll
+template <typename T>
+__device__ __forceinline__ T merge32(T list, T asc, int lane) {
+  T v = list > asc ? list : asc;
+#pragma unroll 1
   for (int o = 16; o > 0; o /= 2) {
-    const uint64_t w = shfl_xor64(v, o);
+    const T w = __shfl_xor_sync(0xffffffffu, v, o);
     v = ((lane & o) == 0) == (v > w) ? v : w;
   }
   return v;
@@ -154,87 +260,93 @@ __device__ __forceinline__ uint64_t ld_dsmem_u64(const void* p, uint32_t rank) {
   return v;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobArgs p, int ctas) {
+template <int DT, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThreads)
+    token_logprobs_kernel(const LogprobArgs p, int ctas) {
   using E = Elem<DT>;
-  constexpr int kN = E::kN;
+  constexpr int kN = E::kN, kWarps = kThreads / 32;
   __shared__ uint64_t buffers[kWarps][kBuffer];
-  __shared__ uint32_t counts[kWarps];
   __shared__ uint64_t lists[kWarps][32];
   __shared__ float sums[kWarps][3];
   __shared__ uint32_t before[kWarps];
+  __shared__ uint32_t tops[kWarps][32];  // the threads' maxima, sorted by warps
   __shared__ struct {
     uint64_t list[32];
     float m, s, t;
     uint32_t before;
   } cta;
+  const float kInf = __uint_as_float(0x7F800000u), kNan = __uint_as_float(0x7FC00000u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = (int)(blockIdx.x % (unsigned)ctas);
   const int64_t row = blockIdx.x / (unsigned)ctas;
   const int K = p.topk;
   pdl_launch_dependents();
-  if (lane == 0) counts[warp] = 0;
-  __syncwarp();
   pdl_wait();
   const typename E::T* z = static_cast<const typename E::T*>(p.logits) + row * p.ld;
   const int vocab = (int)p.vocab;
+  // the row as `head` elements up to a 16-byte boundary, `vectors` of 16 bytes, and a tail; the
+  // vectors in groups of kU per lane
+  constexpr int kU = 4;
+  const int head = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(z) & 15)) % 16 / sizeof(typename E::T)));
+  const int vectors = (vocab - head) / kN;
+  const uint4* const zv = reinterpret_cast<const uint4*>(z + head);
+  const int groups = (vectors + 32 * kU - 1) / (32 * kU), step = ctas * kWarps;
+  // a warp's groups in ascending order, then, for one warp of the row, the elements of both ends
+  // (lanes 0 and 8 on, one each) as a group of their own
+  const bool ends = part == 0 && warp == 0;
+  const int first = part * kWarps + warp;
+  const int mine = first < groups ? (groups - first + step - 1) / step : 0;
+  const int rounds = mine + (ends ? 1 : 0);
+  const int groups_all = groups / step + (groups % step >= (part + 1) * kWarps ? 1 : 0);  // that every warp here has
+  uint4 q[kU];
+  auto load_group = [&](int round) {  // what is behind the last vector reads as masked
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t v = ((int64_t)(first + round * step) * kU + u) * 32 + lane;
+      q[u] = round < mine && v < vectors ? ldg_stream_v4(zv + v)
+                                         : make_uint4(E::kMasked, E::kMasked, E::kMasked, E::kMasked);
+    }
+  };
+  if (rounds > 0) load_group(0);
+
   const int64_t token = p.tokens[row];
   const bool has_token = token >= 0 && token < p.vocab;
   const float zt = has_token ? E::one(z, token) : 0.0f;
   const uint64_t token_key = has_token ? key_of(zt, (uint32_t)token) : 0;
-
-  // vector v covers elements [v kN - shift, + kN): 16-byte aligned in memory
-  const int shift = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(typename E::T));
-  const int64_t vectors = ((int64_t)vocab + shift + kN - 1) / kN;
+  // behind the token a greater value comes before it, ahead of it an equal one too
+  const uint32_t lim_behind = E::spread(zt), lim_ahead = E::before(zt);
 
   Sums a{kFloor, 0.0f, 0.0f};
-  uint32_t earlier = 0;                      // entries before the token
-  uint64_t list = 0;                         // this lane's entry of the warp's best, descending by lane
-  uint64_t least = 0;                        // the K-th of them
-  float above = K > 0 ? __uint_as_float(0x7FC00000u) : __uint_as_float(0x7F800000u);  // its value; NaN: none yet
+  uint32_t earlier = 0;                 // entries before the token
+  uint64_t list = 0;                    // this lane's entry of the warp's best, descending by lane
+  uint64_t least = 0;                   // the K-th of them
+  uint32_t count = 0;                   // keys in the warp's buffer
+  float above = K > 0 ? kNan : kInf;    // a value not above this cannot enter the list (NaN: any can)
 
-  auto flush = [&](uint32_t count) {  // merge `count` buffered keys into the list
-    for (uint32_t i = 0; i < count; i += 32) {
-      const uint64_t v = i + lane < count ? buffers[warp][i + lane] : 0;
-      list = merge32(list, sort32(v, lane), lane);
-    }
-    least = __shfl_sync(0xffffffffu, list, K - 1);
-    if (least != 0) above = value_of((uint32_t)(least >> 32));
-    __syncwarp();
-    if (lane == 0) counts[warp] = 0;
-    __syncwarp();
-  };
-
-  const int64_t step = (int64_t)ctas * kThreads;
-  const int64_t warp0 = (int64_t)part * kThreads + warp * 32;
-  for (int64_t v0 = warp0; v0 < vectors; v0 += step) {
-    const int64_t v = v0 + lane;
-    const int e0 = (int)(v * kN) - shift;
-    uint32_t w[4] = {0, 0, 0, 0};
-    const bool whole = v < vectors && e0 >= 0 && e0 + kN <= vocab;
-    if (whole) {
-      const uint4 q = ldg_stream_v4(z + e0);
-      w[0] = q.x;
-      w[1] = q.y;
-      w[2] = q.z;
-      w[3] = q.w;
-    }
-    float x[kN];
+#pragma unroll 1
+  for (int round = 0; round < rounds; ++round) {
+    uint32_t w[kU][4];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) x[i] = E::get(w, i);
-    uint32_t valid = (1u << kN) - 1;
-    if (!whole) {  // the row's ends, element by element; what is outside it counts as masked
-      valid = 0;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const bool in = v < vectors && e0 + i >= 0 && e0 + i < vocab;
-        x[i] = in ? E::one(z, e0 + i) : __uint_as_float(0xFF800000u);
-        valid |= in ? 1u << i : 0;
-      }
+    for (int u = 0; u < kU; ++u) {
+      w[u][0] = q[u].x;
+      w[u][1] = q[u].y;
+      w[u][2] = q[u].z;
+      w[u][3] = q[u].w;
     }
-    float mx = x[0];
+    int end_index = -1;  // this lane's element of an end
+    if (round == mine) {
+      const int tail = vocab - head - vectors * kN;
+      if (lane < head && lane < 8) end_index = lane;
+      if (lane >= 8 && lane - 8 < tail) end_index = vocab - tail + lane - 8;
+      if (end_index >= 0) w[0][0] = E::raw(z, end_index);
+    }
+    if (round + 1 < rounds) load_group(round + 1);
+    uint32_t mw = w[0][0];
 #pragma unroll
-    for (int i = 1; i < kN; ++i) mx = max_nan(mx, x[i]);
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mw = E::wmax(mw, w[u][i]);
+    const float mx = E::top(mw);
     if (mx > a.m) {
       const float d = max_nan(a.m - mx, kFar);
       const float c = exp2_fast(d * kLog2e);
@@ -242,48 +354,179 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
       a.s = c * a.s;
       a.m = mx;
     }
+    // masked elements: an exponential of 0, or of 1 while the thread has seen nothing above
+    // kFloor, which the first value above it, or another thread's, multiplies by 0
+    const uint64_t minus_m = pack2(-a.m, -a.m), l2e = pack2(kLog2e, kLog2e);
+    uint64_t s2 = pack2(a.s, 0.0f), t2 = pack2(a.t, 0.0f);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float d = max_nan(x[i], kFloor) - a.m;
-      const float e = exp2_fast(d * kLog2e);
-      a.s += valid >> i & 1 ? e : 0.0f;
-      a.t = fmaf(d, valid >> i & 1 ? e : 0.0f, a.t);
+    for (int u = 0; u < kU; ++u) {
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = E::lift(w[u][i]);
+#pragma unroll
+      for (int i = 0; i < kN; i += 2) {
+        float x = E::get(c, i), y = E::get(c, i + 1);
+        if (DT == FI_DTYPE_F16) {
+          x = max_nan(x, kFloor);
+          y = max_nan(y, kFloor);
+        }
+        const uint64_t d = add2(pack2(x, y), minus_m);
+        float ex, ey;
+        unpack2(mul2(d, l2e), ex, ey);
+        const uint64_t e = pack2(exp2_fast(ex), exp2_fast(ey));
+        s2 = add2(s2, e);
+        t2 = fma2(d, e, t2);
+      }
     }
-    if (has_token && !(mx < zt)) {
+    float lo, hi;
+    unpack2(s2, lo, hi);
+    a.s = lo + hi;
+    unpack2(t2, lo, hi);
+    a.t = lo + hi;
+
+    bool around = false;
+    if (has_token) {
+      // this lane's elements, first to last: all behind the token, all ahead of it, or around it
+      const int64_t g0 = (int64_t)(first + round * step) * kU * 32 + lane;
+      const int64_t low = round == mine ? (end_index >= 0 ? end_index : 0) : head + g0 * kN;
+      const int64_t high = round == mine ? low + 1 : low + ((kU - 1) * 32 + 1) * kN;
+      if (zt > -kInf && (token < low || token >= high)) {
+        const uint32_t limit = token < low ? lim_behind : lim_ahead;
+        uint32_t n = 0;
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        earlier += (valid >> i & 1) && key_of(x[i], (uint32_t)(e0 + i)) > token_key ? 1 : 0;
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) E::count(n, w[u][i], limit);
+        earlier += E::counted(n);
+      } else {
+        around = true;  // one by one, as for a token of NaN or -inf
+      }
     }
-    // buffer what is above the warp's K-th (a NaN compares as above)
-    const bool any = K > 0 && valid != 0 && !(mx <= above);
-    if (__any_sync(0xffffffffu, any)) {
-      if (any) {
+    if (K > 0) {
+      // now and then, while every warp of the CTA still has a group: at least K elements are not
+      // below the K-th of the threads' maxima, so that only a few more than K get past it
+      if ((round == 0 || round == 2 || round == 6 || round == 16) && round < groups_all) {
+        uint32_t v = sort32(a.m > kFloor ? order_of(a.m) : 0u, lane);
+        __syncthreads();
+        tops[warp][31 - lane] = v;
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+          __syncthreads();
+          if (warp < o) tops[warp][lane] = merge32(tops[warp][lane], tops[warp + o][31 - lane], lane);
+        }
+        __syncthreads();
+        const float b = below(value_of(tops[0][K - 1]));
+        if (!(b <= above)) above = b;
+      }
+      // the row's first elements come last here: of equal values they are the earlier ones
+      if (round == mine) above = below(above);
+    }
+    const bool last = round + 1 == rounds;
+    if (__any_sync(0xffffffffu, around || !(mx <= above)) || (last && count > 0)) {
+#pragma unroll 1
+      for (int u = 0; u < kU; ++u) {
+        uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const uint64_t key = key_of(x[i], (uint32_t)(e0 + i));
-          if ((valid >> i & 1) && key > least) buffers[warp][atomicAdd(&counts[warp], 1u)] = key;
+        for (int i = 0; i < 4; ++i) v[i] = u < 2 ? (u == 0 ? w[0][i] : w[1][i]) : (u == 2 ? w[2][i] : w[3][i]);
+        const float mu = E::top(E::wmax(E::wmax(v[0], v[1]), E::wmax(v[2], v[3])));
+        const int at = ((first + round * step) * kU + u) * 32 + lane;
+        const int e0 = round == mine ? end_index : head + at * kN;
+        const uint32_t valid = round == mine ? (u == 0 && end_index >= 0 ? 1u : 0u) : (at < vectors ? (1u << kN) - 1 : 0u);
+        if (around) {
+          if (zt != zt) {  // a NaN token: only a NaN of a lower index comes before it
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              earlier += (valid >> i & 1) && key_of(E::get(v, i), (uint32_t)(e0 + i)) > token_key ? 1 : 0;
+          } else {
+            uint32_t more = 0, same = 0;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              more |= !(E::get(v, i) <= zt) ? 1u << i : 0u;
+              same |= E::get(v, i) == zt ? 1u << i : 0u;
+            }
+            const int64_t ahead = token - e0;  // elements of this vector ahead of the token
+            same &= ahead <= 0 ? 0u : (ahead >= kN ? ~0u : (1u << ahead) - 1);
+            earlier += __popc((more | same) & valid);
+          }
+        }
+        if (K > 0 && (__any_sync(0xffffffffu, !(mu <= above)) || (count > 0 && (last || (u == kU - 1 && (int)count >= K))))) {
+          uint32_t todo = 0;
+          // The limit of before this vector, and equal values too: what a merge on the way brings
+          // into the list may have a higher index than an equal value still to come.
+          const float from = below(above);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) todo |= !(E::get(v, i) <= from) ? 1u << i : 0u;
+          todo &= valid;
+          // few candidates go into the list one by one, many by way of the buffer
+          const bool few = least != 0 && count == 0 && __reduce_add_sync(0xffffffffu, (uint32_t)__popc(todo)) <= 8;
+          for (;;) {
+            uint32_t who = __ballot_sync(0xffffffffu, todo != 0);
+            const int i = __ffs(todo) - 1;  // this lane's next candidate
+            float x = E::get(v, 0);
+#pragma unroll
+            for (int j = 1; j < kN; ++j) x = i == j ? E::get(v, j) : x;
+            const uint64_t key = key_of(x, (uint32_t)(e0 + i));
+            if (few) {
+              if (!who) break;
+              for (; who; who &= who - 1) {
+                const uint64_t k = __shfl_sync(0xffffffffu, key, __ffs(who) - 1);
+                if (k > least) {
+                  const int place = __popc(__ballot_sync(0xffffffffu, list > k));
+                  const uint64_t prev = __shfl_up_sync(0xffffffffu, list, 1);
+                  list = lane < place ? list : (lane == place ? k : prev);
+                  least = __shfl_sync(0xffffffffu, list, K - 1);
+                }
+              }
+            } else {
+              if (todo) buffers[warp][count + __popc(who & ((1u << lane) - 1))] = key;
+              count += __popc(who);
+              // a list's worth at a group's end: the limit it brings spares the next groups this path
+              const bool rest = !who && u == kU - 1 && count > 0 && ((int)count >= K || last);
+              if (count >= 32 || rest) {
+                __syncwarp();
+                const uint32_t here = min(count, 32u);  // the buffer is never beyond 63
+                const uint64_t k = (uint32_t)lane < here ? buffers[warp][lane] : 0;
+                const uint64_t left = (uint32_t)lane + 32 < count ? buffers[warp][lane + 32] : 0;
+                __syncwarp();
+                buffers[warp][lane] = left;
+                count -= here;
+                list = merge32(list, sort32(k, lane), lane);
+                least = __shfl_sync(0xffffffffu, list, K - 1);
+                __syncwarp();
+              }
+              if (!who && !(rest && count > 0)) break;
+            }
+            todo &= todo - 1;
+          }
+          if (least != 0) {
+            const float own = value_of((uint32_t)(least >> 32));
+            if (!(own <= above)) above = own;
+                }
         }
       }
-      __syncwarp();
-      const uint32_t count = counts[warp];
-      if (count >= 32) flush(count);
     }
   }
-  if (K > 0) {
-    __syncwarp();
-    flush(counts[warp]);
-    lists[warp][lane] = list;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
-    // the same order on both sides of the exchange, so that all lanes agree in every bit
-    a = lane & o ? join(b, a) : join(a, b);
-    earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
-  }
+  if (K > 0) lists[warp][lane] = list;
+  auto join_lanes = [&](int lanes) {  // the sums and counts of the first `lanes` lanes, in every lane
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+      Sums b;
+      b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+      b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+      b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
+      // the same order on both sides of the exchange, so that all lanes agree in every bit
+      a = lane & o ? join(b, a) : join(a, b);
+      earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
+    }
+  };
+  auto merge_lists = [&](int n) {  // the first n lists (a power of two), into warp 0's
+    for (int o = n / 2; o > 0; o >>= 1) {
+      __syncthreads();
+      if (warp < o) {
+        list = merge32(lists[warp][lane], lists[warp + o][31 - lane], lane);
+        lists[warp][lane] = list;
+      }
+    }
+  };
+  join_lanes(32);
   if (lane == 0) {
     sums[warp][0] = a.m;
     sums[warp][1] = a.s;
@@ -291,15 +534,15 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
     before[warp] = earlier;
   }
   __syncthreads();
+  if (K > 0) merge_lists(kWarps);
   if (warp == 0) {
-    a = Sums{sums[0][0], sums[0][1], sums[0][2]};
-    earlier = before[0];
-    for (int w = 1; w < kWarps; ++w) {
-      a = join(a, Sums{sums[w][0], sums[w][1], sums[w][2]});
-      earlier += before[w];
-      if (K > 0) list = merge32(list, lists[w][31 - lane], lane);
-    }
-    if (ctas > 1) {
+    const int w = lane % kWarps;
+    a = Sums{sums[w][0], sums[w][1], sums[w][2]};
+    earlier = before[w];
+    join_lanes(kWarps);
+  }
+  if (ctas > 1) {
+    if (warp == 0) {
       cta.list[lane] = list;
       if (lane == 0) {
         cta.m = a.m;
@@ -308,21 +551,22 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
         cta.before = earlier;
       }
     }
-  }
-  if (ctas > 1) {
     __syncwarp();
     cluster_sync();
-    if (part == 0 && warp == 0) {
-      for (int r = 1; r < ctas; ++r) {
-        a = join(a, Sums{__uint_as_float(ld_dsmem_u32(&cta.m, r)), __uint_as_float(ld_dsmem_u32(&cta.s, r)),
-                         __uint_as_float(ld_dsmem_u32(&cta.t, r))});
-        earlier += ld_dsmem_u32(&cta.before, r);
-        if (K > 0) list = merge32(list, ld_dsmem_u64(&cta.list[31 - lane], r), lane);
+    if (part == 0) {
+      if (K > 0 && warp < ctas) lists[warp][lane] = ld_dsmem_u64(&cta.list[lane], (uint32_t)warp);
+      if (warp == 0) {
+        const uint32_t r = (uint32_t)(lane % ctas);
+        a = Sums{__uint_as_float(ld_dsmem_u32(&cta.m, r)), __uint_as_float(ld_dsmem_u32(&cta.s, r)),
+                 __uint_as_float(ld_dsmem_u32(&cta.t, r))};
+        earlier = ld_dsmem_u32(&cta.before, r);
+        join_lanes(ctas);
       }
     }
     __syncwarp();
     cluster_sync();  // no CTA leaves while its sums are read
     if (part != 0) return;
+    if (K > 0) merge_lists(ctas);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -383,14 +627,8 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobA
   }
 }
 
-template <int DT>
-int launch(const LogprobArgs& a, cudaStream_t stream) {
-  // CTAs per row: as many as leave each at least 4 vectors per thread, while the rows alone do
-  // not give every SM its CTAs
-  const int64_t vectors = a.vocab / Elem<DT>::kN;
-  int ctas = 1;
-  while (ctas < 8 && a.rows * ctas * 2 <= (int64_t)device_sm_count() * 4 && vectors >= (int64_t)ctas * 2 * kThreads * 4)
-    ctas *= 2;
+template <int DT, int kThreads>
+int launch(const LogprobArgs& a, int ctas, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -404,9 +642,22 @@ int launch(const LogprobArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT>, a, ctas) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, kThreads>, a, ctas) != cudaSuccess)
     return set_cuda_error("token_logprobs_kernel launch");
   return FI_OK;
+}
+
+template <int DT>
+int launch_rows(const LogprobArgs& a, cudaStream_t stream) {
+  // CTAs per row: as many as leave each a group of vectors per warp, while the rows alone do not
+  // give every SM its CTAs
+  const int64_t groups = a.vocab / Elem<DT>::kN / 128, sms = device_sm_count();
+  const bool few = a.rows * 8 <= sms && groups >= 8 * (kFew / 32) / 2;
+  if (groups < 32 && a.rows >= 8 * sms) return launch<DT, kShort>(a, 1, stream);
+  const int64_t warps = (few ? kFew : kMany) / 32, slots = few ? sms : 4 * sms;
+  int ctas = 1;
+  while (ctas < 8 && a.rows * ctas * 2 <= slots && groups >= ctas * 2 * warps / 2) ctas *= 2;
+  return few ? launch<DT, kFew>(a, ctas, stream) : launch<DT, kMany>(a, ctas, stream);
 }
 
 }  // namespace
@@ -414,11 +665,11 @@ int launch(const LogprobArgs& a, cudaStream_t stream) {
 int launch_token_logprobs(const LogprobArgs& a, int dtype, cudaStream_t stream) {
   switch (dtype) {
     case FI_DTYPE_BF16:
-      return launch<FI_DTYPE_BF16>(a, stream);
+      return launch_rows<FI_DTYPE_BF16>(a, stream);
     case FI_DTYPE_F16:
-      return launch<FI_DTYPE_F16>(a, stream);
+      return launch_rows<FI_DTYPE_F16>(a, stream);
     default:
-      return launch<FI_DTYPE_F32>(a, stream);
+      return launch_rows<FI_DTYPE_F32>(a, stream);
   }
 }
 

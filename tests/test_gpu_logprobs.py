@@ -102,6 +102,23 @@ def test_ties_go_to_the_lower_index(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [2, 1300])
+def test_ties_at_the_ends_of_unaligned_rows(dtype, rows):
+    """Equal greatest values in the first and last elements of rows that start off a 16-byte
+    boundary, against equal ones in the middle."""
+    vocab = 3000
+    big = torch.zeros((rows, vocab + 9)).to(dtype)
+    big[:, 4:4 + vocab] = _logits(rows, vocab, dtype, 12).clamp(max=5)
+    big[:, 5:9] = 6.0
+    big[:, 1500:1520] = 6.0
+    big[:, vocab - 2:vocab + 4] = 6.0
+    for off in (1, 3, 5):
+        z = big.cuda()[:, off:off + vocab]
+        _check(z, torch.full((rows,), vocab - 1).cuda(), 7)
+        _check(z, torch.full((rows,), 1510).cuda(), 32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("vocab", [700, 50000])
 def test_sorted_rows(dtype, vocab):
     """The worst orders for a running list: every element is a new best, or the first ones stay."""
