@@ -31,7 +31,7 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// 16 bytes of input as fp32 (DT = fi_dtype).
+// 16 bytes of input (DT = fi_dtype): as fp32, and the greatest magnitude in them.
 template <int DT>
 struct Vec;
 template <>
@@ -42,6 +42,10 @@ struct Vec<FI_DTYPE_F32> {
     x[1] = __uint_as_float(v.y);
     x[2] = __uint_as_float(v.z);
     x[3] = __uint_as_float(v.w);
+  }
+  __device__ static float amax(const uint4 v) {
+    return max_nan(max_nan(fabsf(__uint_as_float(v.x)), fabsf(__uint_as_float(v.y))),
+                   max_nan(fabsf(__uint_as_float(v.z)), fabsf(__uint_as_float(v.w))));
   }
 };
 template <>
@@ -55,6 +59,15 @@ struct Vec<FI_DTYPE_BF16> {
       x[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
     }
   }
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static float amax(const uint4 v) {
+    const uint32_t m = 0x7FFF7FFFu, w = max2(max2(v.x & m, v.y & m), max2(v.z & m, v.w & m));
+    return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
 };
 template <>
 struct Vec<FI_DTYPE_F16> {
@@ -67,23 +80,83 @@ struct Vec<FI_DTYPE_F16> {
       x[2 * q + 1] = f16_hi_to_f32(w[q]);
     }
   }
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static float amax(const uint4 v) {
+    const uint32_t m = 0x7FFF7FFFu, w = max2(max2(v.x & m, v.y & m), max2(v.z & m, v.w & m));
+    return max_nan(f16_lo_to_f32(w), f16_hi_to_f32(w));
+  }
 };
 
-__device__ __forceinline__ float block_scale(float amax) { return __fdiv_rn(amax, 448.0f); }
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// A block's scale and what its divisions need. Where the scale is far from the ends of the fp32
+// range, x / scale is found as Markstein's theorem allows ("Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990): with y the correctly rounded reciprocal and q within
+// one unit of the quotient, q + (x - q scale) y rounds to the correctly rounded quotient. The
+// first product may be two units off, so it takes two such steps: five packed instructions for
+// two elements, where two IEEE divisions are several times that. All signs are turned, so that
+// -0 keeps its own.
+struct Scale {
+  float s;
+  uint64_t ss, my;  // (s, s), (-1 / s, -1 / s)
+  bool plain;       // IEEE divisions
+};
+
+__device__ __forceinline__ Scale block_scale(float amax) {
+  Scale r;
+  r.s = __fdiv_rn(amax, 448.0f);
+  r.plain = !(r.s > 0x1p-90f && r.s < 0x1p90f);
+  const float y = -__frcp_rn(r.s);
+  r.ss = pack2(r.s, r.s);
+  r.my = pack2(y, y);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t quotient_codes(float x0, float x1, const Scale& s) {
+  const uint64_t x = pack2(x0, x1);
+  uint64_t q;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(s.my));
+  q = fma2(fma2(q, s.ss, x), s.my, q);
+  q = fma2(fma2(q, s.ss, x), s.my, q);
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(q));
+  return f32x2_to_e4m3x2(lo, hi);  // of the negative quotients
+}
 
 // kN codes of one 16-byte vector, stored at dst.
 template <int DT>
-__device__ __forceinline__ void store_codes(const uint4 v, float scale, uint8_t* dst) {
+__device__ __forceinline__ void store_codes(const uint4 v, const Scale& s, uint8_t* dst) {
   constexpr int kN = Vec<DT>::kN;
   float x[kN];
   Vec<DT>::unpack(v, x);
   uint32_t w[kN / 4];
+  if (!s.plain) {
 #pragma unroll
-  for (int i = 0; i < kN / 4; ++i) {
-    w[i] = 0;
-    if (scale != 0.0f)
-      w[i] = f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
-             (f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16);
+    for (int i = 0; i < kN / 4; ++i)
+      w[i] = (quotient_codes(x[4 * i], x[4 * i + 1], s) | (quotient_codes(x[4 * i + 2], x[4 * i + 3], s) << 16)) ^
+             0x80808080u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i) {
+      w[i] = 0;
+      if (s.s != 0.0f)
+        w[i] = f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], s.s), __fdiv_rn(x[4 * i + 1], s.s)) |
+               (f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], s.s), __fdiv_rn(x[4 * i + 3], s.s)) << 16);
+    }
   }
   if constexpr (kN == 8)
     *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
@@ -91,19 +164,10 @@ __device__ __forceinline__ void store_codes(const uint4 v, float scale, uint8_t*
     *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
-template <int DT>
-__device__ __forceinline__ float vec_amax(const uint4 v) {
-  float x[Vec<DT>::kN];
-  Vec<DT>::unpack(v, x);
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < Vec<DT>::kN; ++i) m = max_nan(m, fabsf(x[i]));
-  return m;
-}
-
 // One group per 128 / kN lanes (16 lanes for 16-bit elements, a warp for fp32), U groups per
-// lane so that U loads are in flight.
-template <int DT, int U>
+// lane so that U loads are in flight. WHOLE: k is a multiple of 128, so that the groups follow one
+// another in memory and no row has to be found.
+template <int DT, int U, bool WHOLE>
 __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const uint8_t* __restrict__ x, int64_t groups,
                                                              uint32_t kblocks, int64_t k, uint8_t* __restrict__ q,
                                                              float* __restrict__ scale) {
@@ -111,28 +175,31 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const uint8_t* __re
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % kLanes;
-  const int64_t per_cta = 256 / kLanes;
-  const int64_t g0 = (int64_t)blockIdx.x * per_cta * U + threadIdx.x / kLanes;
+  constexpr int kPerCta = 256 / kLanes;
+  const int64_t g0 = (int64_t)blockIdx.x * kPerCta * U + threadIdx.x / kLanes;
   uint4 v[U];
+  int64_t at[U];  // this lane's first element of the group; -1 behind the row's end
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t g = g0 + u * per_cta;
-    const int64_t row = g / kblocks, e = (g - row * kblocks) * kFp8Block + lane * kN;
+    const int64_t g = g0 + u * kPerCta;
+    if (WHOLE) {
+      at[u] = g < groups ? g * kFp8Block + lane * kN : -1;
+    } else {
+      const int64_t row = groups <= 0x7fffffff ? (uint32_t)g / kblocks : g / kblocks;
+      const int64_t e = (g - row * kblocks) * kFp8Block + lane * kN;
+      at[u] = g < groups && e < k ? row * k + e : -1;
+    }
     v[u] = make_uint4(0, 0, 0, 0);
-    if (g < groups && e < k) v[u] = ldg_stream_v4(x + (row * k + e) * kEs);
+    if (at[u] >= 0) v[u] = ldg_stream_v4(x + at[u] * kEs);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t g = g0 + u * per_cta;
-    const int64_t row = g / kblocks, e = (g - row * kblocks) * kFp8Block + lane * kN;
-    float m = vec_amax<DT>(v[u]);
+    float m = Vec<DT>::amax(v[u]);
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float s = block_scale(m);
-    if (g < groups) {
-      if (e < k) store_codes<DT>(v[u], s, q + row * k + e);
-      if (lane == 0) scale[g] = s;
-    }
+    const Scale s = block_scale(m);
+    if (at[u] >= 0) store_codes<DT>(v[u], s, q + at[u]);
+    if (lane == 0 && g0 + u * kPerCta < groups) scale[g0 + u * kPerCta] = s.s;
   }
 }
 
@@ -155,7 +222,7 @@ __global__ void __launch_bounds__(512) fp8_quant_square_kernel(const uint8_t* __
     if (r < rows && e < k) v[u] = ldg_stream_v4(x + (r * k + e) * kEs);
   }
 #pragma unroll
-  for (int u = 0; u < kU; ++u) m = max_nan(m, vec_amax<DT>(v[u]));
+  for (int u = 0; u < kU; ++u) m = max_nan(m, Vec<DT>::amax(v[u]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   __shared__ float warp_max[16];
@@ -164,13 +231,13 @@ __global__ void __launch_bounds__(512) fp8_quant_square_kernel(const uint8_t* __
   m = warp_max[threadIdx.x & 15];
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float s = block_scale(m);
+  const Scale s = block_scale(m);
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int64_t r = r0 + u * kStep;
     if (r < rows && e < k) store_codes<DT>(v[u], s, q + r * k + e);
   }
-  if (threadIdx.x == 0) scale[blockIdx.x] = s;
+  if (threadIdx.x == 0) scale[blockIdx.x] = s.s;
 }
 
 template <int DT>
@@ -198,8 +265,10 @@ int launch_quantize(const uint8_t* x, int64_t rows, int64_t k, bool square, uint
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, deep ? fp8_quant_rows_kernel<DT, 4> : fp8_quant_rows_kernel<DT, 1>, x, groups,
-                         (uint32_t)kb, k, q, scale) != cudaSuccess)
+  const bool whole = k % kFp8Block == 0;
+  auto kern = deep ? (whole ? fp8_quant_rows_kernel<DT, 4, true> : fp8_quant_rows_kernel<DT, 4, false>)
+                   : (whole ? fp8_quant_rows_kernel<DT, 1, true> : fp8_quant_rows_kernel<DT, 1, false>);
+  if (cudaLaunchKernelEx(&cfg, kern, x, groups, (uint32_t)kb, k, q, scale) != cudaSuccess)
     return set_cuda_error("fp8_quant_rows_kernel launch");
   return FI_OK;
 }

@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
     if (K > 0) {
       // now and then, while every warp of the CTA still has a group: at least K elements are not
       // below the K-th of the threads' maxima, so that only a few more than K get past it
-      if ((round == 0 || round == 2 || round == 6 || round == 16) && round < groups_all) {
+      if ((round == 0 || round == 3) && round < groups_all) {
         uint32_t v = sort32(a.m > kFloor ? order_of(a.m) : 0u, lane);
         __syncthreads();
         tops[warp][31 - lane] = v;
