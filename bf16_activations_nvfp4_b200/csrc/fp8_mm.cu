@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kTileRows = 128;                     // weight rows per tile (the MMA's M)
 constexpr uint32_t kTileBytes = kTileRows * 128;   // a tile of one k block
-constexpr int kScaleSlots = 8;                     // blocks the scale warp may be ahead
+constexpr int kGroup = 4, kGroups = 2;             // blocks of k whose scales share a barrier; groups in the ring
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi0 = 3;
 constexpr int kMaxStages = 10;
 
@@ -54,8 +54,8 @@ struct Geo {
   static constexpr int kTmemCols = 512 / kCtas < kTiles * N * 4 ? 512 / kCtas : kTiles * N * 4;
   static constexpr int kBufs = kTmemCols / (kTiles * N);  // blocks the tensor core may be ahead
   static constexpr uint32_t kBudget = kCtas == 2 ? 112 * 1024 : 226 * 1024;
-  static constexpr uint32_t kScaleBytes = kScaleSlots * kTiles * N * 4;
-  static constexpr uint32_t kFixed = 1024 + kScaleBytes + (2 * kMaxStages + 2 * kBufs + 2 * kScaleSlots + 1) * 8 + 64;
+  static constexpr uint32_t kScaleBytes = kGroups * kGroup * kTiles * N * 4;
+  static constexpr uint32_t kFixed = 1024 + kScaleBytes + (2 * kMaxStages + kBufs + 2 * kGroups + 1) * 8 + 64;
   static constexpr int kStages =
       (kBudget - kFixed) / kStageBytes < kMaxStages ? (kBudget - kFixed) / kStageBytes : kMaxStages;
   static constexpr uint32_t kRing = kStages * kStageBytes;
@@ -78,12 +78,11 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
   uint8_t* const basep = smem_raw + (base - raw_s);
   float* const scales = reinterpret_cast<float*>(basep + G::kRing);  // [slot][tile][N]
   uint64_t* const full = reinterpret_cast<uint64_t*>(basep + G::kRing + G::kScaleBytes);
-  uint64_t* const empty = full + G::kStages;
-  uint64_t* const tmem_full = empty + G::kStages;
-  uint64_t* const tmem_empty = tmem_full + G::kBufs;
+  uint64_t* const done = full + G::kStages;  // a block's MMAs are complete: its stage may be refilled, its sums read
+  uint64_t* const tmem_empty = done + G::kStages;
   uint64_t* const scale_full = tmem_empty + G::kBufs;
-  uint64_t* const scale_empty = scale_full + kScaleSlots;
-  uint64_t* const drain = scale_empty + kScaleSlots;
+  uint64_t* const scale_empty = scale_full + kGroups;
+  uint64_t* const drain = scale_empty + kGroups;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = p.splits;
@@ -99,13 +98,12 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     abort_flag = 0;
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&done[i], 1);
     }
     for (int i = 0; i < G::kBufs; ++i) {
-      mbar_init(&tmem_full[i], 1);
       mbar_init(&tmem_empty[i], G::kEpiWarps);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&scale_full[i], 1);
       mbar_init(&scale_empty[i], G::kEpiWarps);
     }
@@ -126,12 +124,20 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
 
   if (warp == kWarpTma) {
     if (lane == 0) {
+      prefetch_map(&tmap_w0);
+      if (GATED) prefetch_map(&tmap_w1);
+      prefetch_map(&tmap_a);
+      // while the kernel before this one ends: the first weights on their way to L2
+      for (int i = 0; i < KB && i < G::kStages; ++i) {
+        tma_prefetch_2d(&tmap_w0, (kb0 + i) * kFp8Block, (int)(tile_n * kTileRows));
+        if (GATED) tma_prefetch_2d(&tmap_w1, (kb0 + i) * kFp8Block, (int)(tile_n * kTileRows));
+      }
       pdl_wait();
       int issued = 0;
       for (int i = 0; i < KB && !p.debug_stall; ++i) {
         const int st = i % G::kStages;
         if (i >= G::kStages &&
-            !mbar_wait_spin(&empty[st], ((i / G::kStages) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u))
+            !mbar_wait_spin(&done[st], ((i / G::kStages) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u))
           break;
         const uint32_t dst = base + (uint32_t)st * G::kStageBytes;
         const int x = (kb0 + i) * kFp8Block;
@@ -168,8 +174,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
           for (int s = 0; s < 4; ++s)  // K = 32 bytes each
             umma_f8(d, adesc + (uint64_t)(2 * s), bdesc + (uint64_t)(2 * s), idesc, s > 0);
         }
-        umma_commit(&empty[st]);
-        umma_commit(&tmem_full[b]);
+        umma_commit(&done[st]);
       }
       if (!ok) {  // the MMAs in flight end before TMEM is freed
         volatile int never = 0;
@@ -194,29 +199,26 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     };
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) load(d, d);
+    static_assert(kAhead == kGroup, "a group is one batch of loads");
     bool ok = true;
-    for (int i0 = 0; i0 < KB && ok; i0 += kAhead) {
+    for (int i0 = 0; i0 < KB && ok; i0 += kGroup) {
+      const int g = i0 / kGroup % kGroups;
+      if (i0 >= kGroups * kGroup)
+        ok = mbar_wait_spin(&scale_empty[g], (i0 / (kGroup * kGroups) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      float* dst = scales + g * (kGroup * G::kTiles * N);
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        const int i = i0 + d;
-        if (i < KB && ok) {
-          const int sl = i % kScaleSlots;
-          if (i >= kScaleSlots)
-            ok = mbar_wait_spin(&scale_empty[sl], ((i / kScaleSlots) - 1) & 1, &abort_flag, p.timeout_ns, p.err, 2u);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            float* dst = scales + sl * (G::kTiles * N);
+      for (int d = 0; d < kGroup; ++d) {
 #pragma unroll
-            for (int t = 0; t < G::kTiles; ++t)
+        for (int t = 0; t < G::kTiles; ++t)
 #pragma unroll
-              for (int r = 0; r < kPer; ++r)
-                if (lane + 32 * r < N) dst[t * N + lane + 32 * r] = sa[d][r] * sw[d][t];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&scale_full[sl]);
-            load(i + kAhead, d);
-          }
-        }
+          for (int r = 0; r < kPer; ++r)
+            if (lane + 32 * r < N) dst[(d * G::kTiles + t) * N + lane + 32 * r] = sa[d][r] * sw[d][t];
+        load(i0 + kGroup + d, d);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&scale_full[g]);
     }
   } else {
     const int epi = warp - kWarpEpi0, quarter = warp & 3, group = epi >> 2;
@@ -226,52 +228,67 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     float acc[G::kCols];
 #pragma unroll
     for (int c = 0; c < G::kCols; ++c) acc[c] = 0.0f;
-    bool ok = true;
+    // A wait that runs out raises the abort flag; the ones after it then give up quickly, and the
+    // blocks' sums are what TMEM held. So the loop needs no way out.
+    const uint32_t done0 = smem_addr(done), done_end = done0 + G::kStages * 8;
+    const uint32_t sp0 = smem_addr(scales) + (uint32_t)(tile * N + c0) * 4;
+    uint32_t done_bar = done0, phase = 0, ready = 0;
+#pragma unroll 1
     for (int i = 0; i < KB; ++i) {
-      const int b = i % G::kBufs, sl = i % kScaleSlots;
-      ok = mbar_wait_spin(&scale_full[sl], (i / kScaleSlots) & 1, &abort_flag, p.timeout_ns, p.err, 16u) &&
-           mbar_wait_spin(&tmem_full[b], (i / G::kBufs) & 1, &abort_flag, p.timeout_ns, p.err, 16u);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      const int b = i % G::kBufs;
+      if (i % kGroup == 0)
+        mbar_wait_spin(&scale_full[i / kGroup % kGroups], i / (kGroup * kGroups) & 1, &abort_flag, p.timeout_ns, p.err,
+                       16u);
+      if (!ready) mbar_wait_addr(done_bar, phase, &abort_flag, p.timeout_ns, p.err, 16u);
+      __syncwarp();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      done_bar += 8;
+      if (done_bar == done_end) {
+        done_bar = done0;
+        phase ^= 1;
+      }
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)((b * G::kTiles + tile) * N + c0);
-      const float4* sp = reinterpret_cast<const float4*>(scales + sl * (G::kTiles * N) + tile * N + c0);
+      const uint32_t sp = sp0 + (uint32_t)(i % (kGroup * kGroups)) * (G::kTiles * N * 4);
+      constexpr int kChunk = G::kCols == 32 || G::kCols == 64 ? 32 : 16;
 #pragma unroll
-      for (int c = 0; c < G::kCols; c += 16) {
-        uint32_t d[16];
-        tmem_ld16_async(taddr + c, d);
+      for (int c = 0; c < G::kCols; c += kChunk) {
+        uint32_t d[kChunk];
+        tmem_ld_async(taddr + c, d);
         tmem_wait_ld(d);
+        if (c + kChunk == G::kCols) {
+          // everything is in registers: the buffer is free; the next block's barrier is looked at
+          // while this one's last columns are added
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tmem_empty[b]);
+          ready = mbar_peek(done_bar, phase);
+        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 s4 = sp[c / 4 + q];
-          acc[c + 4 * q] = fmaf(__uint_as_float(d[4 * q]), s4.x, acc[c + 4 * q]);
-          acc[c + 4 * q + 1] = fmaf(__uint_as_float(d[4 * q + 1]), s4.y, acc[c + 4 * q + 1]);
-          acc[c + 4 * q + 2] = fmaf(__uint_as_float(d[4 * q + 2]), s4.z, acc[c + 4 * q + 2]);
-          acc[c + 4 * q + 3] = fmaf(__uint_as_float(d[4 * q + 3]), s4.w, acc[c + 4 * q + 3]);
+        for (int q = 0; q < kChunk; q += 4) {
+          uint64_t s01, s23;
+          asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(s01), "=l"(s23) : "r"(sp + (uint32_t)(c + q) * 4));
+          fma_scaled(acc[c + q], acc[c + q + 1], d[q], d[q + 1], s01);
+          fma_scaled(acc[c + q + 2], acc[c + q + 3], d[q + 2], d[q + 3], s23);
         }
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&tmem_empty[b]);
-        mbar_arrive(&scale_empty[sl]);
+      if (i % kGroup == kGroup - 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scale_empty[i / kGroup % kGroups]);
       }
     }
-    if (ok) {
-      if (!GATED && S == 1) {
-        const int64_t j = tile_n * kTileRows + wrow;
-        if (j < p.n) {
-#pragma unroll
-          for (int c = 0; c < G::kCols; ++c)
-            if (c0 + c < rows) store_out(p.out, p.out_dtype, (m0 + c0 + c) * p.n + j, acc[c]);
-        }
-      } else {
-        // the ring is free: every copy has landed and every MMA has read its operands
-        float* part = reinterpret_cast<float*>(basep) + (tile * N + c0) * kTileRows + wrow;
+    if (!GATED && S == 1) {
+      const int64_t j = tile_n * kTileRows + wrow;
+      if (j < p.n) {
 #pragma unroll
         for (int c = 0; c < G::kCols; ++c)
-          if (c0 + c < rows) part[c * kTileRows] = acc[c];
+          if (c0 + c < rows) store_out(p.out, p.out_dtype, (m0 + c0 + c) * p.n + j, acc[c]);
       }
+    } else {
+      // the ring is free: every copy has landed and every MMA has read its operands
+      float* part = reinterpret_cast<float*>(basep) + (tile * N + c0) * kTileRows + wrow;
+#pragma unroll
+      for (int c = 0; c < G::kCols; ++c)
+        if (c0 + c < rows) part[c * kTileRows] = acc[c];
     }
   }
 

@@ -91,29 +91,7 @@ __device__ __forceinline__ void mbar_arrive_remote_if(uint32_t yes, uint32_t add
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-
-// Keeps uses of registers that an earlier tmem_wait32 covered below it.
+// Keeps uses of registers that an earlier tmem_wait_ld covered below it.
 __device__ __forceinline__ void tmem_pass32(uint32_t (&r)[32]) {
   asm volatile(""
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -459,24 +437,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c0 = s0, c1 = s1;
         // 64 columns at a time in two loads: the buffer is held for two load latencies
         uint32_t d0[32], d1[32];
-        tmem_ld32(taddr, d0);
-        tmem_ld32(taddr + 32, d1);
-        tmem_wait32(d0);
+        tmem_ld_async(taddr, d0);
+        tmem_ld_async(taddr + 32, d1);
+        tmem_wait_ld(d0);
         tmem_pass32(d1);
 #pragma unroll
         for (int q = 0; q < 32; q += 2) fma_pair(acc[q], acc[q + 1], d0[q], d0[q + 1], c0);
-        tmem_ld32(taddr + 128, d0);
+        tmem_ld_async(taddr + 128, d0);
 #pragma unroll
         for (int q = 0; q < 32; q += 2) fma_pair(acc[32 + q], acc[33 + q], d1[q], d1[q + 1], c0);
-        tmem_ld32(taddr + 160, d1);
-        tmem_wait32(d0);
+        tmem_ld_async(taddr + 160, d1);
+        tmem_wait_ld(d0);
         tmem_pass32(d1);
         // everything is in registers: the buffer, and at a group's end its scales, are free
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         mbar_arrive_remote_if(first, empty0 + b * 8);
         // the next block's barrier and scales are looked at while this one's columns are added
-        ready = mbar_test(done_bar, phase);
+        ready = mbar_peek(done_bar, phase);
         if (i + 1 < KB) load_scales(it + 1);
         if (it % kGroup == kGroup - 1 && first) mbar_arrive(&scale_empty[it / kGroup % kGroups]);
         ++it;
