@@ -41,6 +41,7 @@ constexpr uint32_t kTileBytes = kTileRows * 128;   // a tile of one k block
 constexpr int kGroup = 4, kGroups = 2;             // blocks of k whose scales share a barrier; groups in the ring
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi0 = 3;
 constexpr int kMaxStages = 10;
+constexpr int kMaxSplits = 8;                      // CTAs of a portable cluster
 
 // The geometry of one instance: N activation rows per tile, one weight tile or two (gated).
 template <int N, bool GATED>
@@ -249,7 +250,8 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       }
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)((b * G::kTiles + tile) * N + c0);
       const uint32_t sp = sp0 + (uint32_t)(i % (kGroup * kGroups)) * (G::kTiles * N * 4);
-      constexpr int kChunk = G::kCols == 32 || G::kCols == 64 ? 32 : 16;
+      // columns in flight from TMEM: all of them where the registers allow it
+      constexpr int kChunk = G::kCols == 64 ? (G::kCtas == 1 ? 64 : 32) : (G::kCols == 32 ? 32 : 16);
 #pragma unroll
       for (int c = 0; c < G::kCols; c += kChunk) {
         uint32_t d[kChunk];
@@ -296,19 +298,38 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
   if (GATED || S > 1) {
     __syncwarp();
     cluster_sync();
-    const int total = rows * kTileRows;
-    const int chunk = ((total + S - 1) / S + 31) / 32 * 32;
-    const int e_end = min(total, (split + 1) * chunk);
-    for (int e = split * chunk + (int)threadIdx.x; e < e_end; e += G::kThreads) {
-      const int64_t j = tile_n * kTileRows + (e & (kTileRows - 1));
-      float v[G::kTiles];
+    // four outputs of one activation row at a time: all splits' sums are on their way before the
+    // first is added
+    const int quads = rows * (kTileRows / 4);
+    const int chunk = (quads + S - 1) / S;
+    const int q_end = min(quads, (split + 1) * chunk);
+    const bool wide = p.n % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+    for (int e = split * chunk + (int)threadIdx.x; e < q_end; e += G::kThreads) {
+      const int64_t j = tile_n * kTileRows + (e & (kTileRows / 4 - 1)) * 4;
+      float4 v[G::kTiles];
 #pragma unroll
       for (int t = 0; t < G::kTiles; ++t) {
-        const uint32_t a = base + (uint32_t)(t * N * kTileRows + e) * 4u;
-        v[t] = ld_dsmem(a, 0);
-        for (int r = 1; r < S; ++r) v[t] = __fadd_rn(v[t], ld_dsmem(a, (uint32_t)r));
+        const uint32_t at = base + (uint32_t)(t * N * kTileRows + e * 4) * 4u;
+        float4 part[kMaxSplits];
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          if (r < S) part[r] = ld_dsmem_v4(at, (uint32_t)r);
+        v[t] = part[0];
+#pragma unroll
+        for (int r = 1; r < kMaxSplits; ++r) {
+          if (r < S) {
+            v[t].x = __fadd_rn(v[t].x, part[r].x);
+            v[t].y = __fadd_rn(v[t].y, part[r].y);
+            v[t].z = __fadd_rn(v[t].z, part[r].z);
+            v[t].w = __fadd_rn(v[t].w, part[r].w);
+          }
+        }
       }
-      if (j < p.n) store_out(p.out, p.out_dtype, (m0 + e / kTileRows) * p.n + j, GATED ? silu(v[0]) * v[G::kTiles - 1] : v[0]);
+      if (GATED) {
+        const float4 u = v[G::kTiles - 1];
+        v[0] = make_float4(silu(v[0].x) * u.x, silu(v[0].y) * u.y, silu(v[0].z) * u.z, silu(v[0].w) * u.w);
+      }
+      if (j < p.n) store_out4(p.out, p.out_dtype, (m0 + e / (kTileRows / 4)) * p.n + j, v[0], wide, p.n - j);
     }
     __syncwarp();
     cluster_sync();  // no CTA leaves while another reads its sums
@@ -336,7 +357,7 @@ int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
   const int64_t slots = (int64_t)sms * G::kCtas;
   int64_t best = -1;
   a.splits = 1;
-  for (int s = 1; s <= 8 && s <= a.kblocks; s *= 2) {
+  for (int s = 1; s <= kMaxSplits && s <= a.kblocks; s *= 2) {
     const int64_t cost = ((units * s + slots - 1) / slots) * ((a.kblocks + s - 1) / s + 6) + (s > 1 ? 4 : 0);
     if (best < 0 || cost < best) {
       best = cost;

@@ -113,6 +113,16 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_async(uint32_t taddr, uint32_t (&r)[64]) {
+  tmem_ld_async(taddr, *reinterpret_cast<uint32_t(*)[32]>(r));
+  tmem_ld_async(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+}
+
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[64]) {
+  tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(r));
+  tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(r + 32));  // at once: nothing is under way any more
+}
+
 // (x, y) += (a, b) * (s.x, s.y), both lanes of one packed instruction.
 __device__ __forceinline__ void fma_scaled(float& x, float& y, uint32_t a, uint32_t b, uint64_t s) {
   asm("{\n .reg .b64 d, f;\n mov.b64 d, {%2, %3};\n mov.b64 f, {%0, %1};\n fma.rn.f32x2 f, d, %4, f;\n"
@@ -125,12 +135,14 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// fp32 at `addr` (a shared-memory address of this CTA) in the cluster's CTA `rank`.
-__device__ __forceinline__ float ld_dsmem(uint32_t addr, uint32_t rank) {
+// Four fp32 at `addr` (a shared-memory address of this CTA) in the cluster's CTA `rank`.
+__device__ __forceinline__ float4 ld_dsmem_v4(uint32_t addr, uint32_t rank) {
   uint32_t remote;
-  float v;
+  float4 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote));
   return v;
 }
 
@@ -139,6 +151,23 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t at, floa
     static_cast<float*>(out)[at] = v;
   else
     static_cast<uint16_t*>(out)[at] = f32_to_out(v, dtype == FI_DTYPE_F16);
+}
+
+// Up to four consecutive outputs (`left` of them inside the row); wide: aligned, one store.
+__device__ __forceinline__ void store_out4(void* out, int dtype, int64_t at, float4 v, bool wide, int64_t left) {
+  if (wide && left >= 4) {
+    if (dtype == FI_DTYPE_F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+          dtype == FI_DTYPE_F16 ? make_uint2(f32x2_to_f16x2(v.x, v.y), f32x2_to_f16x2(v.z, v.w))
+                                : make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+    return;
+  }
+  store_out(out, dtype, at, v.x);
+  if (left > 1) store_out(out, dtype, at + 1, v.y);
+  if (left > 2) store_out(out, dtype, at + 2, v.z);
+  if (left > 3) store_out(out, dtype, at + 3, v.w);
 }
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
