@@ -345,6 +345,9 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
 
 // ---------------------------------------------------------------------------- host side
 
+// Launched never: stands for the kernels' shape in the occupancy query.
+__global__ void shape_kernel() {}
+
 template <int N, bool GATED>
 int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
   using G = Geo<N, GATED>;
@@ -352,13 +355,53 @@ int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
   const int64_t tiles_n = (a.n + kTileRows - 1) / kTileRows;
   a.tiles_m = (int)((a.m + N - 1) / N);
   const int64_t units = tiles_n * a.tiles_m;
-  // the split of least cost: waves of CTAs, each of its blocks of k and a start and an end worth
+  auto kern = fp8_mm_kernel<N, GATED>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return set_cuda_error("cudaGetDevice");
+  static std::atomic<int> active[kMaxDevices][kMaxSplits + 1];  // clusters of s CTAs the device holds at once; [0]: set up
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = G::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (!active[dev][0]) {
+    constexpr int kSame = (int)G::kSmem + 1024;  // with the kernel's static shared memory
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget + 1024) !=
+            cudaSuccess)
+      return set_cuda_error("cudaFuncSetAttribute(fp8 smem)");
+    // The query answers one CTA per SM for a kernel that allocates TMEM, where the device holds as
+    // many as TMEM and shared memory allow: asked for a kernel of the same shape without TMEM.
+    cfg.dynamicSmemBytes = kSame;
+    for (int s = 1; s <= kMaxSplits; ++s) {
+      // a cluster lies within one GPU processing cluster, so fewer fit than SMs / s
+      int n = 0;
+      attr[0].val.clusterDim.x = (unsigned)s;
+      cfg.gridDim = dim3((unsigned)(s * sms));
+      if (cudaOccupancyMaxActiveClusters(&n, shape_kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = std::max(1, sms * G::kCtas / s);
+      }
+      active[dev][s] = n;
+    }
+    cfg.dynamicSmemBytes = G::kSmem;
+    active[dev][0] = 1;
+  }
+  // the split of least cost: waves of clusters, each of its blocks of k and a start and an end worth
   // about 6 of them, and 4 for the meeting of a cluster
-  const int64_t slots = (int64_t)sms * G::kCtas;
   int64_t best = -1;
   a.splits = 1;
-  for (int s = 1; s <= kMaxSplits && s <= a.kblocks; s *= 2) {
-    const int64_t cost = ((units * s + slots - 1) / slots) * ((a.kblocks + s - 1) / s + 6) + (s > 1 ? 4 : 0);
+  for (int s = 1; s <= kMaxSplits && s <= a.kblocks; ++s) {
+    const int64_t at_once = active[dev][s];
+    const int64_t cost = ((units + at_once - 1) / at_once) * ((a.kblocks + s - 1) / s + 6) + (s > 1 ? 4 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       a.splits = s;
@@ -373,28 +416,8 @@ int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
   for (int t = 0; t < G::kTiles && rc == FI_OK; ++t) rc = encode_codes(&tw[t], a.W[t], a.k, a.n, kTileRows);
   if (rc != FI_OK) return rc;
   if (!GATED) tw[1] = tw[0];
-  auto kern = fp8_mm_kernel<N, GATED>;
-  static std::atomic<bool> configured[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return set_cuda_error("cudaGetDevice");
-  if (!configured[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem) != cudaSuccess)
-      return set_cuda_error("cudaFuncSetAttribute(fp8 smem)");
-    configured[dev] = true;
-  }
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.splits;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
+  attr[0].val.clusterDim.x = (unsigned)a.splits;
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(G::kThreads);
-  cfg.dynamicSmemBytes = G::kSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kern, a, ta, tw[0], tw[1]) != cudaSuccess) return set_cuda_error("fp8_mm_kernel launch");
   return FI_OK;
