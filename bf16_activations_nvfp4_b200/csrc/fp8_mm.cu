@@ -348,39 +348,41 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
 // Launched never: stands for the kernels' shape in the occupancy query.
 __global__ void shape_kernel() {}
 
+// How a call is cut, and what it is expected to take in tenths of a block of the CTA-pair kernel
+// (a block of 128 k of one tile there takes about 0.36 us).
+struct Cut {
+  int splits;
+  int64_t units;  // tiles of weight rows x tiles of activation rows
+  int64_t cost;
+};
+
+// The split of least cost: waves of clusters, each with its blocks of k, a start and an end, and the
+// meeting of a cluster. Measured on B200: a block of N = 256 rows takes 0.72 us, one of the gated
+// N = 128 0.9 us, one of N = 128 0.32 us; a wave's start and end 7 us.
 template <int N, bool GATED>
-int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
+int cut_tiles(const Fp8MmArgs& a, Cut* out) {
   using G = Geo<N, GATED>;
   const int sms = device_sm_count();
-  const int64_t tiles_n = (a.n + kTileRows - 1) / kTileRows;
-  a.tiles_m = (int)((a.m + N - 1) / N);
-  const int64_t units = tiles_n * a.tiles_m;
   auto kern = fp8_mm_kernel<N, GATED>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return set_cuda_error("cudaGetDevice");
   static std::atomic<int> active[kMaxDevices][kMaxSplits + 1];  // clusters of s CTAs the device holds at once; [0]: set up
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(G::kThreads);
-  cfg.dynamicSmemBytes = G::kSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (!active[dev][0]) {
-    constexpr int kSame = (int)G::kSmem + 1024;  // with the kernel's static shared memory
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem) != cudaSuccess ||
         cudaFuncSetAttribute(shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget + 1024) !=
             cudaSuccess)
       return set_cuda_error("cudaFuncSetAttribute(fp8 smem)");
     // The query answers one CTA per SM for a kernel that allocates TMEM, where the device holds as
     // many as TMEM and shared memory allow: asked for a kernel of the same shape without TMEM.
-    cfg.dynamicSmemBytes = kSame;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(G::kThreads);
+    cfg.dynamicSmemBytes = G::kSmem + 1024;  // with the kernel's static shared memory
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     for (int s = 1; s <= kMaxSplits; ++s) {
       // a cluster lies within one GPU processing cluster, so fewer fit than SMs / s
       int n = 0;
@@ -392,21 +394,29 @@ int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
       }
       active[dev][s] = n;
     }
-    cfg.dynamicSmemBytes = G::kSmem;
     active[dev][0] = 1;
   }
-  // the split of least cost: waves of clusters, each of its blocks of k and a start and an end worth
-  // about 6 of them, and 4 for the meeting of a cluster
-  int64_t best = -1;
-  a.splits = 1;
+  constexpr int64_t kBlock = N == 256 ? 20 : (GATED && N == 128 ? 24 : 9);
+  out->units = (a.n + kTileRows - 1) / kTileRows * ((a.m + N - 1) / N);
+  out->cost = -1;
   for (int s = 1; s <= kMaxSplits && s <= a.kblocks; ++s) {
     const int64_t at_once = active[dev][s];
-    const int64_t cost = ((units + at_once - 1) / at_once) * ((a.kblocks + s - 1) / s + 6) + (s > 1 ? 4 : 0);
-    if (best < 0 || cost < best) {
-      best = cost;
-      a.splits = s;
+    const int64_t cost =
+        (out->units + at_once - 1) / at_once * ((a.kblocks + s - 1) / s * kBlock + 200) + (s > 1 ? 40 : 0);
+    if (out->cost < 0 || cost < out->cost) {
+      out->cost = cost;
+      out->splits = s;
     }
   }
+  return FI_OK;
+}
+
+template <int N, bool GATED>
+int launch_tile(Fp8MmArgs a, const Cut& cut, cudaStream_t stream) {
+  using G = Geo<N, GATED>;
+  a.tiles_m = (int)((a.m + N - 1) / N);
+  a.splits = cut.splits;
+  const int64_t units = cut.units;
   const int64_t grid = units * a.splits;
   if (grid > 0x7fffffffLL || a.n > 0x7fffff00LL || a.m > 0x7fffff00LL || a.k > 0x7fffff00LL)
     return set_error(FI_ERR_UNSUPPORTED_SHAPE, "m=%lld n=%lld k=%lld is too large", (long long)a.m, (long long)a.n,
@@ -416,11 +426,39 @@ int launch_tile(Fp8MmArgs a, cudaStream_t stream) {
   for (int t = 0; t < G::kTiles && rc == FI_OK; ++t) rc = encode_codes(&tw[t], a.W[t], a.k, a.n, kTileRows);
   if (rc != FI_OK) return rc;
   if (!GATED) tw[1] = tw[0];
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)a.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = G::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, a, ta, tw[0], tw[1]) != cudaSuccess) return set_cuda_error("fp8_mm_kernel launch");
+  if (cudaLaunchKernelEx(&cfg, fp8_mm_kernel<N, GATED>, a, ta, tw[0], tw[1]) != cudaSuccess) return set_cuda_error("fp8_mm_kernel launch");
   return FI_OK;
+}
+
+// This kernel, or the CTA-pair kernel where that is expected to take less: from the rows of a
+// whole tile on, when its tiles of 256 rows x 256 columns keep enough CTA pairs busy. Measured (us,
+// this kernel / CTA pairs): 256 rows of 34816 x 5120 78.5 / 49.9, of 4096 x 14336 28.7 / 49.1; 512
+// rows of 2048 x 7168 18.5 / 28.5, of 34816 x 5120 154 / 88.5.
+template <int N, bool GATED>
+int launch_cheapest(const Fp8MmArgs& a, cudaStream_t stream) {
+  Cut cut;
+  const int rc = cut_tiles<N, GATED>(a, &cut);
+  if (rc != FI_OK) return rc;
+  if (N == 256 || (GATED && N == 128)) {
+    const int64_t tiles = (a.m + 255) / 256 * ((a.n + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
+    const int64_t pairs = std::max(1, device_sm_count() / 2);
+    if ((tiles + pairs - 1) / pairs * (a.kblocks * 10 + 150) + 90 < cut.cost) return launch_fp8_wide(a, GATED, stream);
+  }
+  return launch_tile<N, GATED>(a, cut, stream);
 }
 
 }  // namespace
@@ -430,18 +468,17 @@ int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream) {
   if (!a.err) return set_cuda_error("cudaGetSymbolAddress(device error word)");
   a.timeout_ns = wait_timeout_ns();
   a.debug_stall = take_debug_stall();
-  if (a.m > 256) return launch_fp8_wide(a, gated, stream);
   if (gated) {
-    if (a.m <= 16) return launch_tile<16, true>(a, stream);
-    if (a.m <= 32) return launch_tile<32, true>(a, stream);
-    if (a.m <= 64) return launch_tile<64, true>(a, stream);
-    return launch_tile<128, true>(a, stream);
+    if (a.m <= 16) return launch_cheapest<16, true>(a, stream);
+    if (a.m <= 32) return launch_cheapest<32, true>(a, stream);
+    if (a.m <= 64) return launch_cheapest<64, true>(a, stream);
+    return launch_cheapest<128, true>(a, stream);
   }
-  if (a.m <= 16) return launch_tile<16, false>(a, stream);
-  if (a.m <= 32) return launch_tile<32, false>(a, stream);
-  if (a.m <= 64) return launch_tile<64, false>(a, stream);
-  if (a.m <= 128) return launch_tile<128, false>(a, stream);
-  return launch_tile<256, false>(a, stream);
+  if (a.m <= 16) return launch_cheapest<16, false>(a, stream);
+  if (a.m <= 32) return launch_cheapest<32, false>(a, stream);
+  if (a.m <= 64) return launch_cheapest<64, false>(a, stream);
+  if (a.m <= 128) return launch_cheapest<128, false>(a, stream);
+  return launch_cheapest<256, false>(a, stream);
 }
 
 }  // namespace fi

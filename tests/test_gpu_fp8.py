@@ -217,7 +217,8 @@ def test_empty_products():
     assert bool((fi.mm_fp8_gated(*codes(3, 0, 1), *codes(5, 0, 128), *codes(5, 0, 128), out=out) == 0).all())
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 512, 4096), (16, 4096, 1024), (100, 512, 2048), (700, 512, 1024)])
+@pytest.mark.parametrize("m,n,k", [(1, 512, 4096), (16, 4096, 1024), (100, 512, 2048), (700, 512, 1024),
+                                   (1500, 5000, 512)])
 def test_repeats_bit_for_bit_on_streams_and_in_graphs(m, n, k):
     a = _fp8.cuda(_fp8.quantize(_fp8.normal(m, k, 1, outliers=True), 1))
     w = _fp8.cuda(_fp8.quantize(_fp8.normal(n, k, 2, 0.02), 128))
@@ -268,7 +269,7 @@ def test_a_product_reads_what_the_call_before_it_wrote():
         assert torch.equal(o, ref[i % 3]), i
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 1024, 4096), (200, 512, 1024), (600, 1024, 1024)])
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 4096), (200, 512, 1024), (600, 1024, 1024), (1024, 8192, 1024)])
 @pytest.mark.parametrize("gate", [False, True])
 def test_stalled_producer_reports_timeout_and_recovers(m, n, k, gate):
     a = _fp8.cuda(_fp8.quantize(_fp8.normal(m, k, 1), 1))
