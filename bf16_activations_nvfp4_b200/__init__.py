@@ -17,6 +17,7 @@ lm_head product:
     out = mm_fp8(Aq, As, Wq, Ws)               # bf16 [m, n] (or f16, fp32)
     h = mm_fp8_gated(Aq, As, Gq, Gs, Uq, Us)   # silu(A G^T) * (A U^T)
     lp = token_logprobs(logits, tokens, topk=5)
+    lp = lm_head_logprobs(A, (Wq, Ws), tokens, topk=5)   # or an NVFP4 head (Wq, Ws, g)
 """
 from __future__ import annotations
 
@@ -31,7 +32,7 @@ import torch
 __all__ = [
     "FiError", "KIND_GEMV", "KIND_MMA", "TACTIC_DEFAULT", "make_tactic", "tactic_fields",
     "pack_weights", "mm_bf16_fp4", "splitk_reduce", "quantize_fp8", "pack_weights_fp8", "mm_fp8",
-    "mm_fp8_gated", "token_logprobs", "TokenLogprobs", "MAX_TOPK", "resolve_tactic", "default_tactic",
+    "mm_fp8_gated", "token_logprobs", "lm_head_logprobs", "TokenLogprobs", "FP8_BLOCK", "MAX_TOPK", "resolve_tactic", "default_tactic",
     "list_tactics", "workspace_bytes", "set_workspace", "last_error", "version", "library",
     "library_path", "get_device_error", "debug_set", "DEBUG_STALL_PRODUCER", "DEBUG_WAIT_TIMEOUT_NS",
 ]
@@ -394,7 +395,7 @@ def _quantize(where: str, x: torch.Tensor, name: str, square: bool, out: tuple |
     dev = x.get_device()
     if out is None:
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        s = torch.empty(shape, dtype=torch.float32, device=x.device)
+        s = x.new_empty(shape, dtype=torch.float32)
     else:
         if len(out) != 2:
             raise ValueError("out must be (codes, scale)")
@@ -441,7 +442,7 @@ def _fp8_out(Aq: torch.Tensor, m: int, n: int, out: torch.Tensor | None, out_dty
         raise ValueError(f"the output is bf16, f16 or fp32 (out_dtype {out_dtype}, out "
                          f"{None if out is None else out.dtype})")
     if out is None:
-        return torch.empty((m, n), dtype=dtype, device=Aq.device), dtype
+        return Aq.new_empty((m, n), dtype=dtype), dtype
     _require(out, "out", dtype, 2)
     if out.shape != (m, n):
         raise ValueError(f"out must be [{m}, {n}], got {tuple(out.shape)}")
@@ -514,11 +515,24 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, topk: int = 0) ->
     if tokens.get_device() != dev:
         _same_device(logits, tokens=tokens)
     kk = max(0, min(topk, vocab))
-    device = logits.device
-    lp, ent = torch.empty((2, rows), dtype=torch.float32, device=device).unbind()
+    lp, ent = logits.new_empty((2, rows), dtype=torch.float32).unbind()
     rank = torch.empty_like(tokens)
-    top = torch.empty((rows, kk), dtype=torch.float32, device=device)
+    top = logits.new_empty((rows, kk), dtype=torch.float32)
     ids = torch.empty_like(top, dtype=torch.int64)
     _call("fi_token_logprobs", dev, logits.data_ptr(), _DTYPES_ANY[logits.dtype], rows, vocab, ld, tokens.data_ptr(),
           topk, lp.data_ptr(), ent.data_ptr(), rank.data_ptr(), top.data_ptr(), ids.data_ptr())
     return TokenLogprobs(lp, ent, rank, top, ids)
+
+
+def lm_head_logprobs(A: torch.Tensor, weight: tuple, tokens: torch.Tensor, topk: int = 0) -> TokenLogprobs:
+    """What a server answers with: the lm_head product of the last hidden states A [rows, k]
+    (bf16) and the log probabilities of one token per row. `weight` is an 8-bit head (Wq, Wscale)
+    of pack_weights_fp8, whose logits stay in fp32, or an NVFP4 head (Wq, Wscale, gscale) of
+    pack_weights, whose logits are bf16 (at most 256 rows, as mm_bf16_fp4)."""
+    if len(weight) == 3:
+        logits = mm_bf16_fp4(A, *weight)
+    elif len(weight) == 2:
+        logits = mm_fp8(*quantize_fp8(A), *weight, out_dtype=torch.float32)
+    else:
+        raise ValueError("weight must be (Wq, Wscale) of pack_weights_fp8 or (Wq, Wscale, gscale) of pack_weights")
+    return token_logprobs(logits, tokens, topk)

@@ -326,3 +326,21 @@ def test_feed_forward_and_head_in_a_row():
     assert bool((lp.rank == 0).all()) and torch.equal(lp.top_ids[:, 0], tokens)
     assert bool((lp.logprob.cpu().double() - z.gather(1, tokens.cpu()[:, None])[:, 0]).abs().max() < 1e-5)
     assert bool((lp.top_logprobs.cpu().double() - z.topk(3, 1).values).abs().max() < 1e-5)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 70])
+def test_head_and_answer_of_both_weight_formats(rows):
+    """lm_head_logprobs is the head product and the answer to its logits, for 8-bit and 4-bit heads."""
+    vocab, k = 1003, 512
+    x = _fp8.normal(rows, k, 1).to(torch.bfloat16).cuda()
+    w = _fp8.normal(vocab, k, 2, 0.05).cuda()
+    tokens = (torch.arange(rows) * 13 % vocab).cuda()
+    w8, w4 = fi.pack_weights_fp8(w), fi.pack_weights(w)
+    for weight, logits in ((w8, fi.mm_fp8(*fi.quantize_fp8(x), *w8, out_dtype=torch.float32)), (w4, fi.mm_bf16_fp4(x, *w4))):
+        got, ref = fi.lm_head_logprobs(x, weight, tokens, topk=4), fi.token_logprobs(logits, tokens, topk=4)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        z = torch.log_softmax(logits.double(), 1)
+        assert bool((got.logprob.double() - z.gather(1, tokens[:, None])[:, 0]).abs().max() < 1e-5)
+        assert torch.equal(got.top_ids[:, 0], logits.float().argmax(1))
+    with pytest.raises(ValueError):
+        fi.lm_head_logprobs(x, (w,), tokens)
