@@ -233,14 +233,14 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     // blocks' sums are what TMEM held. So the loop needs no way out.
     const uint32_t done0 = smem_addr(done), done_end = done0 + G::kStages * 8;
     const uint32_t sp0 = smem_addr(scales) + (uint32_t)(tile * N + c0) * 4;
-    uint32_t done_bar = done0, phase = 0, ready = 0;
+    uint32_t done_bar = done0, phase = 0;
 #pragma unroll 1
     for (int i = 0; i < KB; ++i) {
       const int b = i % G::kBufs;
       if (i % kGroup == 0)
         mbar_wait_spin(&scale_full[i / kGroup % kGroups], i / (kGroup * kGroups) & 1, &abort_flag, p.timeout_ns, p.err,
                        16u);
-      if (!ready) mbar_wait_addr(done_bar, phase, &abort_flag, p.timeout_ns, p.err, 16u);
+      mbar_wait_addr(done_bar, phase, &abort_flag, p.timeout_ns, p.err, 16u);
       __syncwarp();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       done_bar += 8;
@@ -258,12 +258,10 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
         tmem_ld_async(taddr + c, d);
         tmem_wait_ld(d);
         if (c + kChunk == G::kCols) {
-          // everything is in registers: the buffer is free; the next block's barrier is looked at
-          // while this one's last columns are added
+          // everything is in registers: the buffer is free
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(&tmem_empty[b]);
-          ready = mbar_peek(done_bar, phase);
         }
 #pragma unroll
         for (int q = 0; q < kChunk; q += 4) {
@@ -278,64 +276,51 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
         if (lane == 0) mbar_arrive(&scale_empty[i / kGroup % kGroups]);
       }
     }
-    if (!GATED && S == 1) {
-      const int64_t j = tile_n * kTileRows + wrow;
-      if (j < p.n) {
+    // the ring is free: every copy has landed and every MMA has read its operands
+    float* part = reinterpret_cast<float*>(basep) + (tile * N + c0) * kTileRows + wrow;
 #pragma unroll
-        for (int c = 0; c < G::kCols; ++c)
-          if (c0 + c < rows) store_out(p.out, p.out_dtype, (m0 + c0 + c) * p.n + j, acc[c]);
-      }
-    } else {
-      // the ring is free: every copy has landed and every MMA has read its operands
-      float* part = reinterpret_cast<float*>(basep) + (tile * N + c0) * kTileRows + wrow;
-#pragma unroll
-      for (int c = 0; c < G::kCols; ++c)
-        if (c0 + c < rows) part[c * kTileRows] = acc[c];
-    }
+    for (int c = 0; c < G::kCols; ++c)
+      if (c0 + c < rows) part[c * kTileRows] = acc[c];
   }
 
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  if (GATED || S > 1) {
-    __syncwarp();
-    cluster_sync();
-    // four outputs of one activation row at a time: all splits' sums are on their way before the
-    // first is added
-    const int quads = rows * (kTileRows / 4);
-    const int chunk = (quads + S - 1) / S;
-    const int q_end = min(quads, (split + 1) * chunk);
-    const bool wide = p.n % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
-    for (int e = split * chunk + (int)threadIdx.x; e < q_end; e += G::kThreads) {
-      const int64_t j = tile_n * kTileRows + (e & (kTileRows / 4 - 1)) * 4;
-      float4 v[G::kTiles];
+  __syncwarp();
+  cluster_sync();
+  // four outputs of one activation row at a time: all splits' sums are on their way before the
+  // first is added
+  const int quads = rows * (kTileRows / 4);
+  const int chunk = (quads + S - 1) / S;
+  const int q_end = min(quads, (split + 1) * chunk);
+  const bool wide = p.n % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  for (int e = split * chunk + (int)threadIdx.x; e < q_end; e += G::kThreads) {
+    const int64_t j = tile_n * kTileRows + (e & (kTileRows / 4 - 1)) * 4;
+    float4 v[G::kTiles];
 #pragma unroll
-      for (int t = 0; t < G::kTiles; ++t) {
-        const uint32_t at = base + (uint32_t)(t * N * kTileRows + e * 4) * 4u;
-        float4 part[kMaxSplits];
+    for (int t = 0; t < G::kTiles; ++t) {
+      const uint32_t at = base + (uint32_t)(t * N * kTileRows + e * 4) * 4u;
+      float4 part[kMaxSplits];
 #pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-          if (r < S) part[r] = ld_dsmem_v4(at, (uint32_t)r);
-        v[t] = part[0];
+      for (int r = 0; r < kMaxSplits; ++r)
+        if (r < S) part[r] = ld_dsmem_v4(at, (uint32_t)r);
+      v[t] = part[0];
 #pragma unroll
-        for (int r = 1; r < kMaxSplits; ++r) {
-          if (r < S) {
-            v[t].x = __fadd_rn(v[t].x, part[r].x);
-            v[t].y = __fadd_rn(v[t].y, part[r].y);
-            v[t].z = __fadd_rn(v[t].z, part[r].z);
-            v[t].w = __fadd_rn(v[t].w, part[r].w);
-          }
+      for (int r = 1; r < kMaxSplits; ++r) {
+        if (r < S) {
+          v[t].x = __fadd_rn(v[t].x, part[r].x);
+          v[t].y = __fadd_rn(v[t].y, part[r].y);
+          v[t].z = __fadd_rn(v[t].z, part[r].z);
+          v[t].w = __fadd_rn(v[t].w, part[r].w);
         }
       }
-      if (GATED) {
-        const float4 u = v[G::kTiles - 1];
-        v[0] = make_float4(silu(v[0].x) * u.x, silu(v[0].y) * u.y, silu(v[0].z) * u.z, silu(v[0].w) * u.w);
-      }
-      if (j < p.n) store_out4(p.out, p.out_dtype, (m0 + e / (kTileRows / 4)) * p.n + j, v[0], wide, p.n - j);
     }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while another reads its sums
-  } else {
-    __syncthreads();
+    if (GATED) {
+      const float4 u = v[G::kTiles - 1];
+      v[0] = make_float4(silu(v[0].x) * u.x, silu(v[0].y) * u.y, silu(v[0].z) * u.z, silu(v[0].w) * u.w);
+    }
+    if (j < p.n) store_out4(p.out, p.out_dtype, (m0 + e / (kTileRows / 4)) * p.n + j, v[0], wide, p.n - j);
   }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another reads its sums
   if (warp == kWarpMma) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)G::kTmemCols)

@@ -22,17 +22,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-// Whether the phase is complete by now, without waiting (try_wait may suspend the thread for microseconds).
-__device__ __forceinline__ uint32_t mbar_peek(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done;
-}
-
 __device__ __forceinline__ bool mbar_wait_addr(uint32_t b, uint32_t parity, volatile int* abort_flag,
                                                uint64_t timeout_ns, unsigned* err_word, unsigned err_bit) {
   uint64_t t0 = 0;

@@ -129,78 +129,61 @@ __device__ __forceinline__ void tile_at(const WideArgs& w, int64_t t, int& tm, i
 }
 
 // One warp's 32 rows x 64 columns of `acc` (from C0 on) to out rows row0.., columns col0..: through
-// 4 KB of shared memory, so that 128 bytes of a row leave together.
-template <int C0>
+// 4 KB of shared memory, so that 128 bytes of a row leave together. Runs once per tile, so what
+// counts is that it is short: its instructions come from far.
+template <int C0, int OUT>
 __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const float (&acc)[128], uint8_t* stage,
                                            int lane, int64_t row0, int64_t col0) {
-  const bool f32 = p.out_dtype == FI_DTYPE_F32, f16 = p.out_dtype == FI_DTYPE_F16;
-  const int es = f32 ? 4 : 2, per = 16 / es;  // elements per 16 bytes
+  constexpr int es = OUT == FI_DTYPE_F32 ? 4 : 2, per = 16 / es;  // elements per 16 bytes
   const uint32_t sbase = smem_addr(stage);
   const int64_t pitch = p.n * es;
   // 16-byte piece ch of row r; the rows' pieces are permuted so that no two lanes meet in a bank
   auto piece = [&](int r, int ch) { return sbase + (uint32_t)(r * 128 + ((ch ^ (r & 7)) * 16)); };
-  auto flush = [&](int64_t col) {
-    __syncwarp();
-    const int r = lane / 8, ch = lane % 8;
-    uint8_t* dst = static_cast<uint8_t*>(p.out) + (row0 + r) * pitch + (col + ch * per) * es;
-    const bool whole = wide && row0 + 32 <= p.m && col + 8 * per <= p.n;
+  constexpr int kStep = 8 * per;  // columns of 128 bytes
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+  for (int c = 0; c < 64; c += kStep) {
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+      const float* a = acc + C0 + c + ch * per;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = OUT == FI_DTYPE_F32 ? __float_as_uint(a[i])
+                                   : (OUT == FI_DTYPE_F16 ? f32x2_to_f16x2(a[2 * i % 8], a[(2 * i + 1) % 8])
+                                                          : f32x2_to_bf16x2(a[2 * i % 8], a[(2 * i + 1) % 8]));
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(lane, ch)), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3])
+                   : "memory");
+    }
+    __syncwarp();
+    const int64_t col = col0 + c + (lane % 8) * per;
+    uint8_t* dst = static_cast<uint8_t*>(p.out) + (row0 + lane / 8) * pitch + col * es;
+    const bool whole = wide && row0 + 32 <= p.m && col0 + c + kStep <= p.n;
+#pragma unroll 1
+    for (int r = lane / 8; r < 32; r += 4) {
       uint4 v;
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(piece(i * 4 + r, ch)));
+                   : "r"(piece(r, lane % 8)));
       if (whole) {
         *reinterpret_cast<uint4*>(dst) = v;
-      } else if (row0 + i * 4 + r < p.m) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (e < per && col + ch * per + e < p.n) {
-            if (f32)
-              reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
-            else
-              reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-          }
+      } else if (row0 + r < p.m) {
+#pragma unroll 1
+        for (int e = 0; e < per && col + e < p.n; ++e) {
+          const uint32_t word = e * es < 8 ? (e * es < 4 ? v.x : v.y) : (e * es < 12 ? v.z : v.w);
+          if (es == 4)
+            reinterpret_cast<uint32_t*>(dst)[e] = word;
+          else
+            reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(e & 1 ? word >> 16 : word);
         }
       }
       dst += 4 * pitch;
     }
     __syncwarp();
-  };
-  auto put = [&](int ch, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(lane, ch)), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-  };
-  if (f32) {
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-#pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
-        const float* a = acc + C0 + c + ch * 4;
-        put(ch, __float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
-      }
-      flush(col0 + c);
-    }
-  } else {
-#pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
-      uint32_t w[4];
-      const float* a = acc + C0 + ch * 8;
-      if (f16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = f32x2_to_f16x2(a[2 * i], a[2 * i + 1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = f32x2_to_bf16x2(a[2 * i], a[2 * i + 1]);
-      }
-      put(ch, w[0], w[1], w[2], w[3]);
-    }
-    flush(col0);
   }
 }
 
-template <bool GATED>
+template <bool GATED, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_wide_kernel(const WideArgs w, const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_w0, const __grid_constant__ CUtensorMap tmap_w1) {
@@ -422,10 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
       load_scales(it);
-      uint32_t ready = 0;
 #pragma unroll 1
       for (int i = 0; i < KB; ++i) {
-        if (!ready) mbar_wait_addr(done_bar, phase, &abort_flag, p.timeout_ns, p.err, 16u);
+        mbar_wait_addr(done_bar, phase, &abort_flag, p.timeout_ns, p.err, 16u);
         __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         done_bar += 8;
@@ -453,8 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         mbar_arrive_remote_if(first, empty0 + b * 8);
-        // the next block's barrier and scales are looked at while this one's columns are added
-        ready = mbar_peek(done_bar, phase);
+        // the next block's scales are read while this one's columns are added
         if (i + 1 < KB) load_scales(it + 1);
         if (it % kGroup == kGroup - 1 && first) mbar_arrive(&scale_empty[it / kGroup % kGroups]);
         ++it;
@@ -470,10 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (GATED) {  // the first 64 columns are gates, the others their up columns
 #pragma unroll
           for (int c = 0; c < 64; ++c) acc[c] = silu(acc[c]) * acc[64 + c];
-          store_rows<0>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128 + half * 64);
+          store_rows<0, OUT>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128 + half * 64);
         } else {
-          store_rows<0>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + half * 64);
-          store_rows<64>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + 128 + half * 64);
+          store_rows<0, OUT>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + half * 64);
+          store_rows<64, OUT>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + 128 + half * 64);
         }
       }
     }
@@ -507,11 +488,18 @@ int launch_fp8_wide(Fp8MmArgs a, bool gated, cudaStream_t stream) {
   for (int t = 0; t < (gated ? 2 : 1) && rc == FI_OK; ++t) rc = encode_codes(&tw[t], a.W[t], a.k, a.n, 128);
   if (rc != FI_OK) return rc;
   if (!gated) tw[1] = tw[0];
-  auto kern = gated ? fp8_wide_kernel<true> : fp8_wide_kernel<false>;
+  const int out = a.out_dtype;
+  auto pick = [&](auto g) {
+    constexpr bool kGated = decltype(g)::value;
+    return out == FI_DTYPE_BF16  ? fp8_wide_kernel<kGated, FI_DTYPE_BF16>
+           : out == FI_DTYPE_F16 ? fp8_wide_kernel<kGated, FI_DTYPE_F16>
+                                 : fp8_wide_kernel<kGated, FI_DTYPE_F32>;
+  };
+  auto kern = gated ? pick(std::true_type{}) : pick(std::false_type{});
   static std::atomic<int> configured[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return set_cuda_error("cudaGetDevice");
-  const int bit = gated ? 2 : 1;
+  const int bit = 1 << (out * 2 + (gated ? 1 : 0));
   if (!(configured[dev] & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
       return set_cuda_error("cudaFuncSetAttribute(fp8 wide smem)");
