@@ -32,6 +32,7 @@ namespace fi {
 namespace {
 
 constexpr int kBuffer = 64;  // keys a warp may hold before it merges: 31, and one of every lane
+constexpr int kMaxCtas = 8;  // of a row: a portable cluster
 constexpr int kShort = 64, kMany = 256, kFew = 1024;  // threads of a CTA: many short rows, many rows, few rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -0x1.2cp126f;  // stands for -inf (0xFE96 in bf16): (kFloor - M) log2 e is finite, its exponential 0
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
     if (K > 0) {
       // now and then, while every warp of the CTA still has a group: at least K elements are not
       // below the K-th of the threads' maxima, so that only a few more than K get past it
-      if ((round == 0 || round == 3) && round < groups_all) {
+      if ((round == 0 || round == 2 || round == 8) && round < groups_all) {
         uint32_t v = sort32(a.m > kFloor ? order_of(a.m) : 0u, lane);
         __syncthreads();
         tops[warp][31 - lane] = v;
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
           for (int i = 0; i < kN; ++i) todo |= !(E::get(v, i) <= from) ? 1u << i : 0u;
           todo &= valid;
           // few candidates go into the list one by one, many by way of the buffer
-          const bool few = least != 0 && count == 0 && __reduce_add_sync(0xffffffffu, (uint32_t)__popc(todo)) <= 8;
+          const bool few = count == 0 && __reduce_add_sync(0xffffffffu, (uint32_t)__popc(todo)) <= 8;
           for (;;) {
             uint32_t who = __ballot_sync(0xffffffffu, todo != 0);
             const int i = __ffs(todo) - 1;  // this lane's next candidate
@@ -652,11 +653,12 @@ int launch_rows(const LogprobArgs& a, cudaStream_t stream) {
   // CTAs per row: as many as leave each a group of vectors per warp, while the rows alone do not
   // give every SM its CTAs
   const int64_t groups = a.vocab / Elem<DT>::kN / 128, sms = device_sm_count();
-  const bool few = a.rows * 8 <= sms && groups >= 8 * (kFew / 32) / 2;
+  const bool few = a.rows * 16 <= sms && groups >= 8 * (kFew / 32) / 2;
   if (groups < 32 && a.rows >= 8 * sms) return launch<DT, kShort>(a, 1, stream);
-  const int64_t warps = (few ? kFew : kMany) / 32, slots = few ? sms : 4 * sms;
+  const int64_t warps = (few ? kFew : kMany) / 32, slots = few ? sms : 768 / kMany * sms;
   int ctas = 1;
-  while (ctas < 8 && a.rows * ctas * 2 <= slots && groups >= ctas * 2 * warps / 2) ctas *= 2;
+  static_assert(kMany / 32 >= kMaxCtas && kFew / 32 >= kMaxCtas, "a warp takes the list of each CTA of a cluster");
+  while (ctas < kMaxCtas && a.rows * ctas * 2 <= slots && groups >= ctas * 2 * warps / 2) ctas *= 2;
   return few ? launch<DT, kFew>(a, ctas, stream) : launch<DT, kMany>(a, ctas, stream);
 }
 
