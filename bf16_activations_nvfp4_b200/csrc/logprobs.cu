@@ -342,12 +342,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
       if (end_index >= 0) w[0][0] = E::raw(z, end_index);
     }
     if (round + 1 < rounds) load_group(round + 1);
-    uint32_t mw = w[0][0];
+    float mu[kU];  // the vectors' maxima
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mw = E::wmax(mw, w[u][i]);
-    const float mx = E::top(mw);
+      mu[u] = E::top(E::wmax(E::wmax(w[u][0], w[u][1]), E::wmax(w[u][2], w[u][3])));
+    const float mx = max_nan(max_nan(mu[0], mu[1]), max_nan(mu[2], mu[3]));
     if (mx > a.m) {
       const float d = max_nan(a.m - mx, kFar);
       const float c = exp2_fast(d * kLog2e);
@@ -423,12 +422,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
     }
     const bool last = round + 1 == rounds;
     if (__any_sync(0xffffffffu, around || !(mx <= above)) || (last && count > 0)) {
+      uint32_t us = last && count > 0 ? 1u << (kU - 1) : 0u, lists_us = 0;  // vectors to look at, for the list
+#pragma unroll
+      for (int u = 0; u < kU; ++u) lists_us |= __any_sync(0xffffffffu, !(mu[u] <= above)) ? 1u << u : 0u;
+      us |= lists_us | (__any_sync(0xffffffffu, around) ? (1u << kU) - 1 : 0u);
 #pragma unroll 1
-      for (int u = 0; u < kU; ++u) {
+      while (us) {
+        const int u = __ffs(us) - 1;
+        us &= us - 1;
         uint32_t v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = u < 2 ? (u == 0 ? w[0][i] : w[1][i]) : (u == 2 ? w[2][i] : w[3][i]);
-        const float mu = E::top(E::wmax(E::wmax(v[0], v[1]), E::wmax(v[2], v[3])));
         const int at = ((first + round * step) * kU + u) * 32 + lane;
         const int e0 = round == mine ? end_index : head + at * kN;
         const uint32_t valid = round == mine ? (u == 0 && end_index >= 0 ? 1u : 0u) : (at < vectors ? (1u << kN) - 1 : 0u);
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
             earlier += __popc((more | same) & valid);
           }
         }
-        if (K > 0 && (__any_sync(0xffffffffu, !(mu <= above)) || (count > 0 && (last || (u == kU - 1 && (int)count >= K))))) {
+        if (K > 0 && ((lists_us >> u & 1) || (!us && count > 0 && (last || (int)count >= K)))) {
           uint32_t todo = 0;
           // The limit of before this vector, and equal values too: what a merge on the way brings
           // into the list may have a higher index than an equal value still to come.
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
               if (todo) buffers[warp][count + __popc(who & ((1u << lane) - 1))] = key;
               count += __popc(who);
               // a list's worth at a group's end: the limit it brings spares the next groups this path
-              const bool rest = !who && u == kU - 1 && count > 0 && ((int)count >= K || last);
+              const bool rest = !who && !us && count > 0 && ((int)count >= K || last);
               if (count >= 32 || rest) {
                 __syncwarp();
                 const uint32_t here = min(count, 32u);  // the buffer is never beyond 63
