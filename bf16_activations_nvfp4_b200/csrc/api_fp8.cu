@@ -118,7 +118,7 @@ int fi_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab
   if (rows == 0) return FI_OK;
   if (vocab == 0) return set_error(FI_ERR_UNSUPPORTED_SHAPE, "an empty vocabulary has no probabilities");
   if (ld < vocab) return set_error(FI_ERR_INVALID_ARG, "ld=%lld is less than vocab=%lld", (long long)ld, (long long)vocab);
-  if (vocab > 0x7fffffe0LL || !product_fits(rows, ld) || rows > 0x0fffffffLL)
+  if (vocab > 0x7fff0000LL || !product_fits(rows, ld) || rows > 0x0fffffffLL)
     return set_error(FI_ERR_UNSUPPORTED_SHAPE, "rows=%lld vocab=%lld is too large", (long long)rows, (long long)vocab);
   if (!logits || !tokens || !logprob || !entropy || !rank || (topk > 0 && (!top_logprobs || !top_ids)))
     return set_error(FI_ERR_INVALID_ARG, "null pointer argument");

@@ -229,14 +229,15 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     float acc[G::kCols];
 #pragma unroll
     for (int c = 0; c < G::kCols; ++c) acc[c] = 0.0f;
-    // A wait that runs out raises the abort flag; the ones after it then give up quickly, and the
-    // blocks' sums are what TMEM held. So the loop needs no way out.
+    // A wait that runs out raises the abort flag; the ones after it then give up at once, and the
+    // blocks' sums are what TMEM held. The flag is looked at now and then.
     const uint32_t done0 = smem_addr(done), done_end = done0 + G::kStages * 8;
     const uint32_t sp0 = smem_addr(scales) + (uint32_t)(tile * N + c0) * 4;
     uint32_t done_bar = done0, phase = 0;
 #pragma unroll 1
     for (int i = 0; i < KB; ++i) {
       const int b = i % G::kBufs;
+      if (i % 64 == 63 && __any_sync(0xffffffffu, abort_flag != 0)) break;
       if (i % kGroup == 0)
         mbar_wait_spin(&scale_full[i / kGroup % kGroups], i / (kGroup * kGroups) & 1, &abort_flag, p.timeout_ns, p.err,
                        16u);

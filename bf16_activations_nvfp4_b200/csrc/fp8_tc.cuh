@@ -28,8 +28,8 @@ __device__ __forceinline__ bool mbar_wait_addr(uint32_t b, uint32_t parity, vola
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
     if (mbar_test(b, parity)) return true;
+    if (i % 16 == 1 && *abort_flag) return false;
     if (i % 256 == 0) {  // reading the clock takes long: not in a wait that is about to end
-      if (*abort_flag) return false;
       const uint64_t t = globaltimer_ns();
       if (t0 == 0) t0 = t;
       if (t - t0 > timeout_ns) {

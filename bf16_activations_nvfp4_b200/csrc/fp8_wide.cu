@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int epi = warp - 4, quarter = warp & 3, half = epi >> 2;
     uint8_t* const stage = staging + epi * (kOutBytes / 8);
     const uint32_t empty0 = map_to(smem_addr(tmem_empty), 0);
-    // A wait that runs out raises the abort flag; the ones after it then give up quickly, and the
-    // blocks' sums are what TMEM held. So the loop below needs no way out.
+    // A wait that runs out raises the abort flag; the ones after it then give up at once, and the
+    // blocks' sums are what TMEM held: the way out is between tiles.
     const uint32_t done0 = smem_addr(done), done_end = done0 + kStages * 8;
     const uint32_t sp0 = smem_addr(scales) + (uint32_t)(quarter * 32 + lane) * 8;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 64);
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    : "=f"(s0), "=f"(s1)
                    : "r"(sp0 + i % (kGroup * kGroups) * (2 * kRows * 4)));
     };
-    for (int64_t t = 0; t < my_tiles; ++t) {
+    for (int64_t t = 0; t < my_tiles && !__any_sync(0xffffffffu, abort_flag != 0); ++t) {
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 32; q += 2) fma_pair(acc[96 + q], acc[97 + q], d1[q], d1[q + 1], c1);
       }
-      if (!abort_flag) {
+      if (!__any_sync(0xffffffffu, abort_flag != 0)) {
         int tm, tn;
         tile_at(w, pair + t * pairs, tm, tn);
         const int64_t row0 = ((int64_t)tm * 2 + rank) * kRows + quarter * 32;

@@ -1,5 +1,8 @@
 """8-bit codes with a scale per block of 128, and their products, on the GPU."""
-import numpy as np
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -344,3 +347,34 @@ def test_head_and_answer_of_both_weight_formats(rows):
         assert torch.equal(got.top_ids[:, 0], logits.float().argmax(1))
     with pytest.raises(ValueError):
         fi.lm_head_logprobs(x, (w,), tokens)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of each operator is captured: what a call sets up once does not
+    break the capture, and the replay gives what the plain calls give afterwards."""
+    code = """
+import torch
+import bf16_activations_nvfp4_b200 as fi
+x = torch.randn(40, 512, device="cuda").bfloat16()
+big = torch.randn(2000, 512, device="cuda").bfloat16()
+w = torch.randn(3000, 512, device="cuda")
+t = torch.zeros(40, dtype=torch.int64, device="cuda")
+def calls():
+    p, a, b = fi.pack_weights_fp8(w), fi.quantize_fp8(x), fi.quantize_fp8(big)
+    y = fi.mm_fp8(*a, *p, out_dtype=torch.float32)
+    return [y, fi.mm_fp8(*b, *p), fi.mm_fp8_gated(*a, *p, *p), fi.mm_fp8_gated(*b, *p, *p), *fi.token_logprobs(y, t, 5)]
+torch.cuda.synchronize()
+s = torch.cuda.Stream()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=s):
+    held = calls()
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(held, calls()):
+    assert torch.equal(a, b)
+assert fi.get_device_error() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
