@@ -189,26 +189,25 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
 
+// Sums relative to a reference point M = m log2 e (rounded to fp32, the same wherever it is
+// formed from m): s = sum of 2^(z log2 e - M), t = sum of (z log2 e - M) times that.
 struct Sums {
-  float m, s, t;  // maximum, sum of 2^((z - m) log2 e), sum of (z - m) times that
+  float m, s, t;
 };
+
+__device__ __forceinline__ float point(float m) { return __fmul_rn(m, kLog2e); }
 
 __device__ __forceinline__ Sums join(const Sums a, const Sums b) {
   Sums r;
   r.m = max_nan(a.m, b.m);
-  const float da = max_nan(a.m - r.m, kFar), db = max_nan(b.m - r.m, kFar);
-  const float ca = exp2_fast(da * kLog2e), cb = exp2_fast(db * kLog2e);
+  const float da = max_nan(point(a.m) - point(r.m), kFar), db = max_nan(point(b.m) - point(r.m), kFar);
+  const float ca = exp2_fast(da), cb = exp2_fast(db);
   r.s = ca * a.s + cb * b.s;
   r.t = ca * (a.t + da * a.s) + cb * (b.t + db * b.s);
   return r;
@@ -300,19 +299,27 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   const int rounds = mine + (ends ? 1 : 0);
   const int groups_all = groups / step + (groups % step >= (part + 1) * kWarps ? 1 : 0);  // that every warp here has
   uint4 q[kU];
-  auto load_group = [&](int round) {  // what is behind the last vector reads as masked
+  const uint4* from = zv + (int64_t)first * 32 * kU + lane;  // of the next group's loads
+  auto load_group = [&](int round) {
+    if ((first + round * step + 1) * (32 * kU) <= vectors) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t v = ((int64_t)(first + round * step) * kU + u) * 32 + lane;
-      q[u] = round < mine && v < vectors ? ldg_stream_v4(zv + v)
-                                         : make_uint4(E::kMasked, E::kMasked, E::kMasked, E::kMasked);
+      for (int u = 0; u < kU; ++u) q[u] = ldg_stream_v4(from + u * 32);
+    } else {  // the row's last group: what is behind the last vector reads as masked
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int v = ((first + round * step) * kU + u) * 32 + lane;
+        q[u] = round < mine && v < vectors ? ldg_stream_v4(from + u * 32)
+                                           : make_uint4(E::kMasked, E::kMasked, E::kMasked, E::kMasked);
+      }
     }
+    from += step * 32 * kU;
   };
   if (rounds > 0) load_group(0);
 
   const int64_t token = p.tokens[row];
   const bool has_token = token >= 0 && token < p.vocab;
   const float zt = has_token ? E::one(z, token) : 0.0f;
+  const int at_token = has_token ? (int)token : -1;
   const uint64_t token_key = has_token ? key_of(zt, (uint32_t)token) : 0;
   // behind the token a greater value comes before it, ahead of it an equal one too
   const uint32_t lim_behind = E::spread(zt), lim_ahead = E::before(zt);
@@ -348,15 +355,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
       mu[u] = E::top(E::wmax(E::wmax(w[u][0], w[u][1]), E::wmax(w[u][2], w[u][3])));
     const float mx = max_nan(max_nan(mu[0], mu[1]), max_nan(mu[2], mu[3]));
     if (mx > a.m) {
-      const float d = max_nan(a.m - mx, kFar);
-      const float c = exp2_fast(d * kLog2e);
+      const float d = max_nan(point(a.m) - point(mx), kFar);
+      const float c = exp2_fast(d);
       a.t = c * (a.t + d * a.s);
       a.s = c * a.s;
       a.m = mx;
     }
     // masked elements: an exponential of 0, or of 1 while the thread has seen nothing above
     // kFloor, which the first value above it, or another thread's, multiplies by 0
-    const uint64_t minus_m = pack2(-a.m, -a.m), l2e = pack2(kLog2e, kLog2e);
+    const float minus = -point(a.m);
+    const uint64_t minus_m = pack2(minus, minus), l2e = pack2(kLog2e, kLog2e);
     uint64_t s2 = pack2(a.s, 0.0f), t2 = pack2(a.t, 0.0f);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -370,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
           x = max_nan(x, kFloor);
           y = max_nan(y, kFloor);
         }
-        const uint64_t d = add2(pack2(x, y), minus_m);
+        const uint64_t d = fma2(pack2(x, y), l2e, minus_m);
         float ex, ey;
-        unpack2(mul2(d, l2e), ex, ey);
+        unpack2(d, ex, ey);
         const uint64_t e = pack2(exp2_fast(ex), exp2_fast(ey));
         s2 = add2(s2, e);
         t2 = fma2(d, e, t2);
@@ -387,11 +395,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
     bool around = false;
     if (has_token) {
       // this lane's elements, first to last: all behind the token, all ahead of it, or around it
-      const int64_t g0 = (int64_t)(first + round * step) * kU * 32 + lane;
-      const int64_t low = round == mine ? (end_index >= 0 ? end_index : 0) : head + g0 * kN;
-      const int64_t high = round == mine ? low + 1 : low + ((kU - 1) * 32 + 1) * kN;
-      if (zt > -kInf && (token < low || token >= high)) {
-        const uint32_t limit = token < low ? lim_behind : lim_ahead;
+      const int low = round == mine ? max(end_index, 0) : head + ((first + round * step) * kU * 32 + lane) * kN;
+      const int high = round == mine ? low + 1 : low + ((kU - 1) * 32 + 1) * kN;
+      if (zt > -kInf && (at_token < low || at_token >= high)) {
+        const uint32_t limit = at_token < low ? lim_behind : lim_ahead;
         uint32_t n = 0;
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
               more |= !(E::get(v, i) <= zt) ? 1u << i : 0u;
               same |= E::get(v, i) == zt ? 1u << i : 0u;
             }
-            const int64_t ahead = token - e0;  // elements of this vector ahead of the token
+            const int ahead = at_token - e0;  // elements of this vector ahead of the token
             same &= ahead <= 0 ? 0u : (ahead >= kN ? ~0u : (1u << ahead) - 1);
             earlier += __popc((more | same) & valid);
           }
@@ -581,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   }
   __syncthreads();
   a = Sums{cta.m, cta.s, cta.t};
-  if (a.m <= kFloor || a.m > 1e38f) {
+  const bool far = a.m <= kFloor || a.m > 1e38f;
+  if (far) {
     // rare: the true maximum first, then sums with clamped differences, by this CTA alone
     float mx = __uint_as_float(0xFF800000u);
     for (int i = threadIdx.x; i < vocab; i += kThreads) mx = max_nan(mx, E::one(z, i));
@@ -619,11 +627,14 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   }
   if (warp != 0) return;
   const bool empty = a.s == 0.0f;  // nothing but -inf
-  const float ln_s = empty ? 0.0f : __log2f(a.s) * kLn2;
-  auto logprob_of = [&](float x) { return empty ? x : (x - a.m) - ln_s; };
+  const float log2_s = empty ? 0.0f : __log2f(a.s), mean = empty ? 0.0f : a.t / a.s;
+  // ln(sum exp(z - m)): the point is off m log2 e by its rounding (of a far row the sums are relative
+  // to the maximum itself, t in natural units)
+  const float ln_sum = (far ? log2_s : log2_s - fmaf(a.m, kLog2e, -point(a.m))) * kLn2;
+  auto logprob_of = [&](float x) { return empty ? x : (x - a.m) - ln_sum; };
   if (lane == 0) {
     p.logprob[row] = has_token ? logprob_of(zt) : __uint_as_float(0x7FC00000u);
-    p.entropy[row] = empty ? 0.0f : ln_s - a.t / a.s;
+    p.entropy[row] = far ? log2_s * kLn2 - mean : (log2_s - mean) * kLn2;
     p.rank[row] = has_token ? (int64_t)earlier : -1;
   }
   if (lane < K) {
