@@ -13,23 +13,26 @@
 //   warp 0    TMA producer: 128 x 128 weight tiles (two for the gated form) and N x 128
 //             activation tiles into a ring, 128-byte swizzled;
 //   warp 1    one thread issues the MMAs (four K = 32 steps per block) and the commits;
-//   warp 2    the scales: As * Ws of a block into a small ring, several blocks ahead;
+//   warp 2    the scales: As * Ws of four blocks at a time, up to eight blocks ahead, into a ring;
 //   warps 3.. epilogue, one thread per weight row (two groups of four warps halve the columns,
-//             or take the gate and the up tile).
+//             or take the gate and the up tile): packed FMAs, two columns each.
 // K splits are the CTAs of one cluster: their fp32 sums meet in distributed shared memory, where
 // each CTA adds a slice of the outputs in split order. No workspace, no atomics, one launch.
 //
-// Every wait is bounded (sync.cuh). On a timeout the roles stop, the producer and the MMA issuer
-// wait, bounded, for what they have in flight, and every thread still meets the barriers.
+// Bound by HBM up to some 128 rows: one row of 4096 x 14336 takes 12.6 us (4.7 TB/s; 3 to 4 us are
+// the pipeline's start and the cluster's end), of 248320 x 5120 184 us (6.9 TB/s), the gated form
+// at 16 rows of 2 x 17408 x 5120 30 us (6.0 TB/s). Up to 64 rows two CTAs share an SM, so that one's
+// loads cover the other's start and end; above, a CTA has the SM's tensor memory to itself. 128 rows
+// of 4096 x 14336 take 17.7 us, 256 rows 28.6.
+//
+// Every wait is bounded. On a timeout the roles stop, the producer and the MMA issuer wait,
+// bounded, for what they have in flight, and every thread still meets the barriers.
 #include <cstdint>
 #include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
 
-#include "common.cuh"
-#include "internal.h"
-#include "sync.cuh"
 #include "fp8_tc.cuh"
 
 namespace fi {
@@ -77,7 +80,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
   const uint32_t raw_s = smem_addr(smem_raw);
   const uint32_t base = (raw_s + 1023u) & ~1023u;
   uint8_t* const basep = smem_raw + (base - raw_s);
-  float* const scales = reinterpret_cast<float*>(basep + G::kRing);  // [slot][tile][N]
+  float* const scales = reinterpret_cast<float*>(basep + G::kRing);  // [group][block][tile][N]
   uint64_t* const full = reinterpret_cast<uint64_t*>(basep + G::kRing + G::kScaleBytes);
   uint64_t* const done = full + G::kStages;  // a block's MMAs are complete: its stage may be refilled, its sums read
   uint64_t* const tmem_empty = done + G::kStages;

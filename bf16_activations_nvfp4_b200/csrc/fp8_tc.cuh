@@ -10,8 +10,8 @@
 
 namespace fi {
 
-// mbar_wait_bounded (sync.cuh) for waits of a few hundred cycles: no time to suspend is named, so a
-// waiting thread is back as soon as the hardware notices the phase; the clock is read now and then.
+// One test of the phase, suspended for as long as the hardware sees fit (microseconds, if the phase
+// does not complete: nothing to look ahead with).
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -22,6 +22,9 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+// mbar_wait_bounded (sync.cuh) for waits of a few hundred cycles: no time to suspend is named, so a
+// waiting thread is back as soon as the hardware notices the phase, and the clock is read only in
+// waits that have taken long. Once the CTA has aborted, the first test that fails is the last.
 __device__ __forceinline__ bool mbar_wait_addr(uint32_t b, uint32_t parity, volatile int* abort_flag,
                                                uint64_t timeout_ns, unsigned* err_word, unsigned err_bit) {
   uint64_t t0 = 0;

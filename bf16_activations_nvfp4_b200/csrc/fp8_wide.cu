@@ -5,16 +5,25 @@
 // activation rows x (128 gate + 128 up rows) in the gated form: one tcgen05.mma of both SMs reads
 // 128 rows of A from each CTA and 128 rows of B from each, so a CTA loads 32 KB per 128 k and
 // feeds 256 columns. Roles of a CTA (12 warps):
-//   warp 0      TMA producer of its 128 A rows and 128 B rows, a ring of 5 stages; the bytes of
+//   warp 0      TMA producer of its 128 A rows and 128 B rows into a ring of 5 stages; the bytes of
 //               both CTAs complete one barrier, in the pair's first CTA;
 //   warp 1      in the first CTA, one thread issues the MMAs for both; the commits arrive in both;
 //   warps 2-3   the scales As * Ws of a block, up to 16 blocks ahead, into a ring;
 //   warps 4-11  epilogue, one thread per activation row and half of the columns (128): a block's
 //               sums, times the row's scale, are added to 128 fp32 registers while the tensor
-//               cores fill the other TMEM buffer. setmaxnreg gives these warps 216 registers.
+//               cores fill the other TMEM buffer. setmaxnreg gives these warps 216 registers. A
+//               warp takes 64 columns of each half, so that in the gated form a thread has the
+//               gates and their up columns.
 // The CTAs are persistent: tiles go round-robin over the pairs, in groups of 8 along m, so that
 // the pairs at work share operand rows in L2; the next tile's blocks start while the last one's
 // outputs are written.
+//
+// Bound by the chain of a block's steps (MMAs, commit, TMEM loads, additions, release: two TMEM
+// buffers are in flight) and, under sustained load, by power: 720 to 750 cycles per block of a pair
+// where the MMAs and loads alone take 638 and the nominal rate is 512. 8192 x 4096 x 14336 takes
+// 404 us (2.4 PFLOP/s), 470 at the power limit; 4096 rows of the gated 2 x 17408 x 5120 685 us.
+// N = 128 instructions with four buffers took 646 us on the former where this form took 504, 16
+// epilogue warps 559 against 450.
 //
 // Every wait is bounded; on a timeout the roles stop and every thread still meets the barriers.
 #include <cstdint>
@@ -35,7 +44,7 @@ constexpr uint32_t kPairBytes = 2 * kStageBytes;                // bytes a full 
 constexpr uint32_t kOutBytes = 32 * 1024;                       // staging of the epilogue: 4 KB per warp
 constexpr uint32_t kScaleBytes = kGroups * kGroup * 2 * kRows * 4;
 constexpr uint32_t kBarBytes = (2 * kStages + kBufs + 2 * kGroups + 1) * 8;
-constexpr int kGroupM = 8;
+constexpr int kGroupM = 8;  // 4, 12, 16 and 32 are within 3%
 constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kScaleBytes + kBarBytes;
 static_assert(32 * 128 <= kOutBytes / 8, "a warp stages 128 bytes of 32 rows");
 constexpr int kEpiRegs = 216, kOtherRegs = 64;
@@ -84,6 +93,9 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 // Arrives on a barrier of the pair. It orders TMEM reads only (a tcgen05 fence precedes it), so the
 // default scope is enough: with cluster scope each arrival is a memory barrier, and the kernel ran
 // at half its speed.
+// Arrives on a barrier of the pair. It orders TMEM reads only (a tcgen05 fence precedes it), so the
+// default scope is enough: at cluster scope each arrival is a memory barrier, and the kernel ran at
+// half its speed.
 __device__ __forceinline__ void mbar_arrive_remote_if(uint32_t yes, uint32_t addr) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %0, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%1];\n}" ::"r"(yes),
@@ -197,8 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* const staging = basep + kStages * kStageBytes;
   float* const scales = reinterpret_cast<float*>(staging + kOutBytes);  // [group][block][row][column half]
   uint64_t* const full = reinterpret_cast<uint64_t*>(staging + kOutBytes + kScaleBytes);
-  // a block's MMAs are complete: its stage may be refilled and its sums read. One commit for both:
-  // a commit takes about 200 cycles and the next one waits for it
+  // a block's MMAs are complete: its stage may be refilled and its sums read (one commit for both)
   uint64_t* const done = full + kStages;
   uint64_t* const tmem_empty = done + kStages;
   uint64_t* const scale_full = tmem_empty + kBufs;

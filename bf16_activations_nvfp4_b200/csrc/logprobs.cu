@@ -7,14 +7,23 @@
 //   top  = the first K of that order.
 //
 // Each thread keeps a running (M, S, T) and rescales when its maximum grows: with the new
-// maximum M', c = exp(M - M'), S' = c S and T' = c (T + (M - M') S). Each warp keeps the best 32
-// keys it has seen, one per lane in order; an element above the K-th of them goes to the warp's
-// buffer in shared memory, and 32 buffered keys at a time are sorted (bitonic, by shuffles) and
-// merged into the list. A key is the value as an order-preserving 32-bit integer above the
-// inverted index, so equal values order by index and every result is the same from run to run.
+// maximum M', c = exp(M - M'), S' = c S and T' = c (T + (M - M') S). The rank counts greater elements
+// by packed comparisons.
+//
+// Each warp keeps the best 32 keys it has seen, one per lane in order. A key is the value as an
+// order-preserving 32-bit integer above the inverted index, so equal values order by index and
+// every result is the same from run to run. Only an element above a limit is looked at: the K-th
+// of the threads' maxima so far (found three times per row by sorting them across the CTA: at least
+// K elements are not below it, and few more are) or the K-th of the warp's own list. A few
+// candidates are inserted one by one; many go to a buffer in shared memory and, 32 at a time, are
+// sorted (bitonic, by shuffles) and merged.
 //
 // A row is one CTA, or one cluster of CTAs when there are few rows; the CTAs' sums and lists
-// meet in distributed shared memory. No workspace, no atomics on global memory.
+// meet in distributed shared memory. No workspace, no atomics.
+//
+// Bound by instruction issue (70% of the slots): 2047 x 152064 bf16 takes 111 us without token or
+// list (5.6 TB/s), 133 with ranks, 186 with 5 alternatives, 265 with 32; one fp32 row of 152064 with
+// 20 takes 15 us, most of it the latency of the sorts and merges.
 //
 // Masked entries: -inf is replaced by a value so low that its exponential is 0 (kFloor), which
 // keeps (z - M) exp(z - M) at 0 instead of NaN. A row whose maximum is not above that value (all
