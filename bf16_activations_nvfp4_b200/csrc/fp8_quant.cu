@@ -9,8 +9,9 @@
 //
 // Both are one pass over the input: a block is held in registers between its maximum and its
 // codes. Element bytes + 1 per element: 8192 x 2688 bf16 takes 14.2 us (4.7 TB/s; 23.1 with IEEE
-// divisions), 8192 x 14336 64 us (5.5 TB/s), weights of 14336 x 4096 bf16 38.6 us (4.6 TB/s), fp32
-// 52.5 us (5.6 TB/s).
+// divisions), 8192 x 14336 64 us (5.5 TB/s), weights of 14336 x 4096 bf16 36.7 us (4.8 TB/s), fp32
+// 52.5 us (5.6 TB/s). The launch bounds keep as many CTAs on an SM as their registers allow, since
+// each CTA's loads and stores alternate.
 #include <cstdint>
 
 #include "common.cuh"
@@ -170,7 +171,7 @@ __device__ __forceinline__ void store_codes(const uint4 v, const Scale& s, uint8
 // lane so that U loads are in flight. WHOLE: k is a multiple of 128, so that the groups follow one
 // another in memory and no row has to be found.
 template <int DT, int U, bool WHOLE>
-__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const uint8_t* __restrict__ x, int64_t groups,
+__global__ void __launch_bounds__(256, DT == FI_DTYPE_F32 ? 4 : 6) fp8_quant_rows_kernel(const uint8_t* __restrict__ x, int64_t groups,
                                                              uint32_t kblocks, int64_t k, uint8_t* __restrict__ q,
                                                              float* __restrict__ scale) {
   constexpr int kN = Vec<DT>::kN, kLanes = kFp8Block / kN, kEs = 16 / kN;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const uint8_t* __re
 
 // One CTA of 512 threads per 128 x 128 block, 32 elements per thread.
 template <int DT>
-__global__ void __launch_bounds__(512) fp8_quant_square_kernel(const uint8_t* __restrict__ x, int64_t rows,
+__global__ void __launch_bounds__(512, DT == FI_DTYPE_F32 ? 2 : 4) fp8_quant_square_kernel(const uint8_t* __restrict__ x, int64_t rows,
                                                                uint32_t kblocks, int64_t k, uint8_t* __restrict__ q,
                                                                float* __restrict__ scale) {
   constexpr int kN = Vec<DT>::kN, kLanes = kFp8Block / kN, kEs = 16 / kN, kU = 32 / kN;
