@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
         tma_prefetch_2d(&tmap_w0, (kb0 + i) * kFp8Block, (int)(tile_n * kTileRows));
         if (GATED) tma_prefetch_2d(&tmap_w1, (kb0 + i) * kFp8Block, (int)(tile_n * kTileRows));
       }
+      const uint64_t once = evict_first_policy();
       pdl_wait();
       int issued = 0;
       for (int i = 0; i < KB && !p.debug_stall; ++i) {
@@ -146,8 +147,9 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
         const uint32_t dst = base + (uint32_t)st * G::kStageBytes;
         const int x = (kb0 + i) * kFp8Block;
         mbar_arrive_expect_tx(&full[st], G::kStageBytes);
-        tma_load_2d(dst, &tmap_w0, x, (int)(tile_n * kTileRows), smem_addr(&full[st]));
-        if (GATED) tma_load_2d(dst + kTileBytes, &tmap_w1, x, (int)(tile_n * kTileRows), smem_addr(&full[st]));
+        tma_load_2d_hint(dst, &tmap_w0, x, (int)(tile_n * kTileRows), smem_addr(&full[st]), once);
+        if (GATED)
+          tma_load_2d_hint(dst + kTileBytes, &tmap_w1, x, (int)(tile_n * kTileRows), smem_addr(&full[st]), once);
         tma_load_2d(dst + G::kTiles * kTileBytes, &tmap_a, x, (int)m0, smem_addr(&full[st]));
         issued = i + 1;
       }
