@@ -21,9 +21,11 @@
 // A row is one CTA, or one cluster of CTAs when there are few rows; the CTAs' sums and lists
 // meet in distributed shared memory. No workspace, no atomics.
 //
-// Bound by instruction issue (70% of the slots): 2047 x 152064 bf16 takes 111 us without token or
-// list (5.6 TB/s), 133 with ranks, 186 with 5 alternatives, 265 with 32; one fp32 row of 152064 with
-// 20 takes 15 us, most of it the latency of the sorts and merges.
+// 2047 x 152064 bf16 takes 102 us without token or list (6.1 TB/s), 120 with ranks, 173 with 5
+// alternatives, 245 with 32: bound by HBM, then by the latency of the lists' steps, during which a
+// warp's next groups are on their way to shared memory (held in registers instead, one group
+// ahead, it was 111, 131, 186 and 262; 1024 x 152064 fp32 with 5 takes 127 us, and took 169). One
+// fp32 row of 152064 with 20 takes 14 us, most of it the latency of the sorts and merges.
 //
 // Masked entries: -inf is replaced by a value so low that its exponential is 0 (kFloor), which
 // keeps (z - M) exp(z - M) at 0 instead of NaN. A row whose maximum is not above that value (all
@@ -31,6 +33,7 @@
 // again with every difference clamped.
 #include <cstdint>
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -42,6 +45,8 @@ namespace {
 
 constexpr int kBuffer = 64;  // keys a warp may hold before it merges: 31, and one of every lane
 constexpr int kMaxCtas = 8;  // of a row: a portable cluster
+constexpr int kSlots = 3;     // groups of vectors per warp that are on their way, or being used
+constexpr int kU = 4;         // vectors of a lane in a group
 constexpr int kShort = 64, kMany = 256, kFew = 1024;  // threads of a CTA: many short rows, many rows, few rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -0x1.2cp126f;  // stands for -inf (0xFE96 in bf16): (kFloor - M) log2 e is finite, its exponential 0
@@ -295,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   const int vocab = (int)p.vocab;
   // the row as `head` elements up to a 16-byte boundary, `vectors` of 16 bytes, and a tail; the
   // vectors in groups of kU per lane
-  constexpr int kU = 4;
   const int head = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(z) & 15)) % 16 / sizeof(typename E::T)));
   const int vectors = (vocab - head) / kN;
   const uint4* const zv = reinterpret_cast<const uint4*>(z + head);
@@ -307,23 +311,29 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   const int mine = first < groups ? (groups - first + step - 1) / step : 0;
   const int rounds = mine + (ends ? 1 : 0);
   const int groups_all = groups / step + (groups % step >= (part + 1) * kWarps ? 1 : 0);  // that every warp here has
-  uint4 q[kU];
-  const uint4* from = zv + (int64_t)first * 32 * kU + lane;  // of the next group's loads
-  auto load_group = [&](int round) {
-    if ((first + round * step + 1) * (32 * kU) <= vectors) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) q[u] = ldg_stream_v4(from + u * 32);
-    } else {  // the row's last group: what is behind the last vector reads as masked
+  // Groups come by asynchronous copies, kSlots - 1 of them ahead, into the warp's ring; a lane reads
+  // what it copied itself, so it waits for nobody else.
+  extern __shared__ __align__(16) uint8_t rings[];
+  const uint32_t ring = smem_addr(rings) + (uint32_t)(warp * kSlots * kU * 32 + lane) * 16;
+  const uint4* from = zv + (int64_t)first * 32 * kU + lane;  // of the next group
+  int next_slot = 0;
+  auto copy_group = [&](int round) {
+    if (round < mine) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int v = ((first + round * step) * kU + u) * 32 + lane;
-        q[u] = round < mine && v < vectors ? ldg_stream_v4(from + u * 32)
-                                           : make_uint4(E::kMasked, E::kMasked, E::kMasked, E::kMasked);
+        if (((first + round * step) * kU + u) * 32 + lane < vectors)
+          asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(
+                           ring + (uint32_t)((next_slot * kU + u) * 32) * 16),
+                       "l"(from + u * 32)
+                       : "memory");
       }
+      from += step * 32 * kU;
+      next_slot = next_slot + 1 == kSlots ? 0 : next_slot + 1;
     }
-    from += step * 32 * kU;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (rounds > 0) load_group(0);
+#pragma unroll
+  for (int i = 0; i < kSlots - 1; ++i) copy_group(i);
 
   const int64_t token = p.tokens[row];
   const bool has_token = token >= 0 && token < p.vocab;
@@ -343,21 +353,33 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
 #pragma unroll 1
   for (int round = 0; round < rounds; ++round) {
     uint32_t w[kU][4];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      w[u][0] = q[u].x;
-      w[u][1] = q[u].y;
-      w[u][2] = q[u].z;
-      w[u][3] = q[u].w;
-    }
     int end_index = -1;  // this lane's element of an end
-    if (round == mine) {
+    if (round < mine) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
+      const uint32_t at = ring + (uint32_t)(round % kSlots * kU * 32) * 16;
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                     : "r"(at + u * 512));
+      if ((first + round * step + 1) * (32 * kU) > vectors) {  // what is behind the last vector counts as masked
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[u][i] = ((first + round * step) * kU + u) * 32 + lane < vectors ? w[u][i] : E::kMasked;
+      }
+    } else {
       const int tail = vocab - head - vectors * kN;
       if (lane < head && lane < 8) end_index = lane;
       if (lane >= 8 && lane - 8 < tail) end_index = vocab - tail + lane - 8;
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[u][i] = E::kMasked;
       if (end_index >= 0) w[0][0] = E::raw(z, end_index);
     }
-    if (round + 1 < rounds) load_group(round + 1);
+    copy_group(round + kSlots - 1);
     float mu[kU];  // the vectors' maxima
 #pragma unroll
     for (int u = 0; u < kU; ++u)
@@ -654,6 +676,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
 
 template <int DT, int kThreads>
 int launch(const LogprobArgs& a, int ctas, cudaStream_t stream) {
+  constexpr int kRings = kThreads * kSlots * kU * 16;
+  static_assert(kRings <= 192 * 1024, "beside the lists in shared memory");
+  static std::atomic<bool> configured[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return set_cuda_error("cudaGetDevice");
+  if (!configured[dev]) {
+    if (cudaFuncSetAttribute(token_logprobs_kernel<DT, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings) !=
+        cudaSuccess)
+      return set_cuda_error("cudaFuncSetAttribute(token_logprobs_kernel)");
+    configured[dev] = true;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -664,6 +697,7 @@ int launch(const LogprobArgs& a, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * ctas));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRings;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
