@@ -19,11 +19,11 @@
 // K splits are the CTAs of one cluster: their fp32 sums meet in distributed shared memory, where
 // each CTA adds a slice of the outputs in split order. No workspace, no atomics, one launch.
 //
-// Bound by HBM up to some 128 rows: one row of 4096 x 14336 takes 12.6 us (4.7 TB/s; 3 to 4 us are
+// Bound by HBM up to some 128 rows: one row of 4096 x 14336 takes 12.2 us (4.8 TB/s; 3 to 4 us are
 // the pipeline's start and the cluster's end), of 248320 x 5120 184 us (6.9 TB/s), the gated form
-// at 16 rows of 2 x 17408 x 5120 30 us (6.0 TB/s). Up to 64 rows two CTAs share an SM, so that one's
-// loads cover the other's start and end; above, a CTA has the SM's tensor memory to itself. 128 rows
-// of 4096 x 14336 take 17.7 us, 256 rows 28.6.
+// at 16 rows of 2 x 17408 x 5120 30 us (6.0 TB/s). Up to 64 rows, and up to 96 where there are
+// tiles enough, two CTAs share an SM, so that one's loads cover the other's start and end; above, a
+// CTA has the SM's tensor memory to itself. 128 rows of 4096 x 14336 take 17.7 us, 256 rows 28.6.
 //
 // Every wait is bounded. On a timeout the roles stop, the producer and the MMA issuer wait,
 // bounded, for what they have in flight, and every thread still meets the barriers.
@@ -54,7 +54,7 @@ struct Geo {
   static constexpr int kThreads = (kWarpEpi0 + kEpiWarps) * 32;
   static constexpr int kCols = !GATED && N > 64 ? N / 2 : N;  // accumulators per epilogue thread
   static constexpr uint32_t kStageBytes = kTiles * kTileBytes + N * 128;
-  static constexpr int kCtas = (GATED ? N <= 32 : N <= 64) ? 2 : 1;  // resident per SM
+  static constexpr int kCtas = (GATED ? N <= 32 : N <= 96) ? 2 : 1;  // resident per SM
   static constexpr int kTmemCols = 512 / kCtas < kTiles * N * 4 ? 512 / kCtas : kTiles * N * 4;
   static constexpr int kBufs = kTmemCols / (kTiles * N);  // blocks the tensor core may be ahead
   static constexpr uint32_t kBudget = kCtas == 2 ? 112 * 1024 : 226 * 1024;
@@ -349,7 +349,8 @@ struct Cut {
 
 // The split of least cost: waves of clusters, each with its blocks of k, a start and an end, and the
 // meeting of a cluster. Measured on B200: a block of N = 256 rows takes 0.72 us, one of the gated
-// N = 128 0.9 us, one of N = 128 0.32 us; a wave's start and end 7 us.
+// N = 128 0.9 us, one of N = 128 0.32 us, one of N = 96 with two CTAs on every SM 0.65 us; a wave's
+// start and end 7 us.
 template <int N, bool GATED>
 int cut_tiles(const Fp8MmArgs& a, Cut* out) {
   using G = Geo<N, GATED>;
@@ -387,7 +388,7 @@ int cut_tiles(const Fp8MmArgs& a, Cut* out) {
     }
     active[dev][0] = 1;
   }
-  constexpr int64_t kBlock = N == 256 ? 20 : (GATED && N == 128 ? 24 : 9);
+  constexpr int64_t kBlock = N == 256 ? 20 : (GATED && N == 128 ? 24 : (N == 96 ? 18 : 9));
   out->units = (a.n + kTileRows - 1) / kTileRows * ((a.m + N - 1) / N);
   out->cost = -1;
   for (int s = 1; s <= kMaxSplits && s <= a.kblocks; ++s) {
@@ -452,6 +453,18 @@ int launch_cheapest(const Fp8MmArgs& a, cudaStream_t stream) {
   return launch_tile<N, GATED>(a, cut, stream);
 }
 
+// 65 to 96 rows: tiles of 96 rows two to an SM, or of 128 rows one to an SM, which take half as long
+// each. The first where there are enough tiles for both places: measured (us, 96 / 128) 77 rows of
+// 10304 x 2688 11.7 / 13.9, 80 of 34816 x 5120 37.3 / 43.3, 96 of 248320 x 5120 280 / 315; 96 of
+// 4096 x 4096 12.0 / 9.7, of 2048 x 7168 11.2 / 9.8.
+int launch_96(const Fp8MmArgs& a, cudaStream_t stream) {
+  Cut two, one;
+  int rc = cut_tiles<96, false>(a, &two);
+  if (rc == FI_OK) rc = cut_tiles<128, false>(a, &one);
+  if (rc != FI_OK) return rc;
+  return two.cost < one.cost ? launch_tile<96, false>(a, two, stream) : launch_tile<128, false>(a, one, stream);
+}
+
 }  // namespace
 
 int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream) {
@@ -468,6 +481,7 @@ int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream) {
   if (a.m <= 16) return launch_cheapest<16, false>(a, stream);
   if (a.m <= 32) return launch_cheapest<32, false>(a, stream);
   if (a.m <= 64) return launch_cheapest<64, false>(a, stream);
+  if (a.m <= 96) return launch_96(a, stream);
   if (a.m <= 128) return launch_cheapest<128, false>(a, stream);
   return launch_cheapest<256, false>(a, stream);
 }

@@ -119,7 +119,8 @@ def test_whole_numbers_are_exact(m, n, k):
     assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all())
 
 
-@pytest.mark.parametrize("m,n,k", [(2500, 5000, 400), (3000, 2501, 128), (257, 20000, 16)])
+@pytest.mark.parametrize("m,n,k", [(2500, 5000, 400), (3000, 2501, 128), (257, 20000, 16), (65, 39001, 272),
+                                   (96, 10304, 2704)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_many_tiles(m, n, k, dtype):
     """More output tiles than the GPU holds at once, with ragged edges, in every type; rows around
@@ -272,7 +273,8 @@ def test_a_product_reads_what_the_call_before_it_wrote():
         assert torch.equal(o, ref[i % 3]), i
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 1024, 4096), (200, 512, 1024), (600, 1024, 1024), (1024, 8192, 1024)])
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 4096), (80, 20480, 1024), (200, 512, 1024), (600, 1024, 1024),
+                                   (1024, 8192, 1024)])
 @pytest.mark.parametrize("gate", [False, True])
 def test_stalled_producer_reports_timeout_and_recovers(m, n, k, gate):
     a = _fp8.cuda(_fp8.quantize(_fp8.normal(m, k, 1), 1))
