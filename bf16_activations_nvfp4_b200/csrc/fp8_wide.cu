@@ -91,9 +91,6 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 }
 
 // Arrives on a barrier of the pair. It orders TMEM reads only (a tcgen05 fence precedes it), so the
-// default scope is enough: with cluster scope each arrival is a memory barrier, and the kernel ran
-// at half its speed.
-// Arrives on a barrier of the pair. It orders TMEM reads only (a tcgen05 fence precedes it), so the
 // default scope is enough: at cluster scope each arrival is a memory barrier, and the kernel ran at
 // half its speed.
 __device__ __forceinline__ void mbar_arrive_remote_if(uint32_t yes, uint32_t addr) {
