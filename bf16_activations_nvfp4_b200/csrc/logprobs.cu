@@ -10,22 +10,24 @@
 // maximum M', c = exp(M - M'), S' = c S and T' = c (T + (M - M') S). The rank counts greater elements
 // by packed comparisons.
 //
-// Each warp keeps the best 32 keys it has seen, one per lane in order. A key is the value as an
-// order-preserving 32-bit integer above the inverted index, so equal values order by index and
-// every result is the same from run to run. Only an element above a limit is looked at: the K-th
-// of the threads' maxima so far (found three times per row by sorting them across the CTA: at least
-// K elements are not below it, and few more are) or the K-th of the warp's own list. A few
-// candidates are inserted one by one; many go to a buffer in shared memory and, 32 at a time, are
-// sorted (bitonic, by shuffles) and merged.
+// Candidates for the list are keys: the value as an order-preserving 32-bit integer above the
+// inverted index, so equal values order by index and every result is the same from run to run.
+// Only an element above a limit becomes one: the K-th of the threads' (or of 32 groups of threads')
+// maxima so far, found up to four times per row, as at least K elements are not below it and few
+// more are. A warp's candidates go to its buffer in shared memory; 32 of them are sorted (bitonic,
+// by shuffles) and merged into its list of the best 32, one per lane. Mostly there are fewer: then
+// those of all warps are put in a row at the end and take one sort.
 //
 // A row is one CTA, or one cluster of CTAs when there are few rows; the CTAs' sums and lists
 // meet in distributed shared memory. No workspace, no atomics.
 //
-// 2047 x 152064 bf16 takes 102 us without token or list (6.1 TB/s), 120 with ranks, 173 with 5
-// alternatives, 245 with 32: bound by HBM, then by the latency of the lists' steps, during which a
-// warp's next groups are on their way to shared memory (held in registers instead, one group
-// ahead, it was 111, 131, 186 and 262; 1024 x 152064 fp32 with 5 takes 127 us, and took 169). One
-// fp32 row of 152064 with 20 takes 14 us, most of it the latency of the sorts and merges.
+// 2047 x 152064 bf16 takes 99 us without token or list (6.3 TB/s), 117 with ranks, 147 with 5
+// alternatives, 212 with 32: bound by HBM, then by instruction issue (61% of the slots, at 14 warps
+// per SM) and the latency of the lists' steps, during which a warp's next groups are on their way to
+// shared memory (held in registers instead, one group ahead, and candidates inserted one by one it
+// was 111, 131, 186 and 262). 1024 x 152064 fp32 with 5 takes 122 us, 4096 x 32000 bf16 with 5 89
+// (inserted one by one: 117). One fp32 row of 152064 with 20 takes 13 us, most of it the latency of
+// the steps at its end (7.5 without the list).
 //
 // Masked entries: -inf is replaced by a value so low that its exponential is 0 (kFloor), which
 // keeps (z - M) exp(z - M) at 0 instead of NaN. A row whose maximum is not above that value (all
@@ -47,7 +49,8 @@ constexpr int kBuffer = 64;  // keys a warp may hold before it merges: 31, and o
 constexpr int kMaxCtas = 8;  // of a row: a portable cluster
 constexpr int kSlots = 3;     // groups of vectors per warp that are on their way, or being used
 constexpr int kU = 4;         // vectors of a lane in a group
-constexpr int kShort = 64, kMany = 256, kFew = 1024;  // threads of a CTA: many short rows, many rows, few rows
+constexpr int kFewTops = 8;   // up to here a limit comes from 32 maxima
+constexpr int kShort = 128, kMany = 256, kFew = 1024;  // threads of a CTA: many short rows, many rows, few rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -0x1.2cp126f;  // stands for -inf (0xFE96 in bf16): (kFloor - M) log2 e is finite, its exponential 0
 constexpr float kFar = -1e30f;    // least difference of two maxima: times a sum it stays finite
@@ -107,7 +110,13 @@ __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// kN elements in four 32-bit words. raw: one element and masked ones in a word; wmax: the greater of two words, element by element; lift: the
+// w[i], i not known at compile time.
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&w)[4], int i) {
+  const uint32_t lo = i & 1 ? w[1] : w[0], hi = i & 1 ? w[3] : w[2];
+  return i & 2 ? hi : lo;
+}
+
+// kN elements in four 32-bit words; get and pick: element i (pick: i not known at compile time). raw: one element and masked ones in a word; wmax: the greater of two words, element by element; lift: the
 // word with its -inf replaced by a value whose exponential is 0 (for f16, once it is fp32);
 // count: n += the word's elements above those of `limit` (NaN is above everything).
 template <int DT>
@@ -118,6 +127,7 @@ struct Elem<FI_DTYPE_F32> {
   static constexpr uint32_t kMasked = 0xFF800000u;  // -inf in every element
   static constexpr int kN = 4;
   __device__ static float get(const uint32_t (&w)[4], int i) { return __uint_as_float(w[i]); }
+  __device__ static float pick(const uint32_t (&w)[4], int i) { return __uint_as_float(word_of(w, i)); }
   __device__ static float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
   __device__ static uint32_t raw(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
   __device__ static uint32_t wmax(uint32_t a, uint32_t b) {
@@ -139,6 +149,10 @@ struct Elem<FI_DTYPE_BF16> {
   static constexpr int kN = 8;
   __device__ static float get(const uint32_t (&w)[4], int i) {
     return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  __device__ static float pick(const uint32_t (&w)[4], int i) {
+    const uint32_t v = word_of(w, i >> 1);
+    return __uint_as_float(i & 1 ? v & 0xFFFF0000u : v << 16);
   }
   __device__ static float one(const void* p, int64_t i) { return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]); }
   __device__ static uint32_t raw(const void* p, int64_t i) {
@@ -170,6 +184,10 @@ struct Elem<FI_DTYPE_F16> {
   static constexpr int kN = 8;
   __device__ static float get(const uint32_t (&w)[4], int i) {
     return i & 1 ? f16_hi_to_f32(w[i / 2]) : f16_lo_to_f32(w[i / 2]);
+  }
+  __device__ static float pick(const uint32_t (&w)[4], int i) {
+    const uint32_t v = word_of(w, i >> 1);
+    return f16_lo_to_f32(i & 1 ? v >> 16 : v);
   }
   __device__ static float one(const void* p, int64_t i) { return f16_lo_to_f32(static_cast<const uint16_t*>(p)[i]); }
   __device__ static uint32_t raw(const void* p, int64_t i) {
@@ -216,16 +234,6 @@ struct Sums {
 };
 
 __device__ __forceinline__ float point(float m) { return __fmul_rn(m, kLog2e); }
-
-__device__ __forceinline__ Sums join(const Sums a, const Sums b) {
-  Sums r;
-  r.m = max_nan(a.m, b.m);
-  const float da = max_nan(point(a.m) - point(r.m), kFar), db = max_nan(point(b.m) - point(r.m), kFar);
-  const float ca = exp2_fast(da), cb = exp2_fast(db);
-  r.s = ca * a.s + cb * b.s;
-  r.t = ca * (a.t + da * a.s) + cb * (b.t + db * b.s);
-  return r;
-}
 
 // The warp's 32 keys, one per lane, into ascending order by lane. (The loops stay loops: the
 // kernel's time goes up with its code, as the instruction caches are small.)
@@ -282,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   __shared__ uint64_t buffers[kWarps][kBuffer];
   __shared__ uint64_t lists[kWarps][32];
   __shared__ float sums[kWarps][3];
-  __shared__ uint32_t before[kWarps];
-  __shared__ uint32_t tops[kWarps][32];  // the threads' maxima, sorted by warps
+  __shared__ uint32_t before[kWarps], pending[kWarps];
+  __shared__ uint32_t tops[kWarps][32];  // the threads' maxima, sorted by warps, or those of 32 groups of threads
   __shared__ struct {
     uint64_t list[32];
     float m, s, t;
@@ -346,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   Sums a{kFloor, 0.0f, 0.0f};
   uint32_t earlier = 0;                 // entries before the token
   uint64_t list = 0;                    // this lane's entry of the warp's best, descending by lane
-  uint64_t least = 0;                   // the K-th of them
   uint32_t count = 0;                   // keys in the warp's buffer
   float above = K > 0 ? kNan : kInf;    // a value not above this cannot enter the list (NaN: any can)
 
@@ -441,29 +448,60 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
       }
     }
     if (K > 0) {
-      // now and then, while every warp of the CTA still has a group: at least K elements are not
-      // below the K-th of the threads' maxima, so that only a few more than K get past it
-      if ((round == 0 || round == 2 || round == 8) && round < groups_all) {
-        uint32_t v = sort32(a.m > kFloor ? order_of(a.m) : 0u, lane);
-        __syncthreads();
-        tops[warp][31 - lane] = v;
-        for (int o = kWarps / 2; o > 0; o >>= 1) {
+      // Now and then, while every warp of the CTA still has a group: at least K elements are not
+      // below the K-th of the threads' maxima, so that only a few more than K get past it. (Where
+      // there are warps without a group, each warp takes its own lanes'.)
+      if ((round == 0 || round == 1 || round == 3 || round == 7) && round < max(groups_all, 1)) {
+        uint32_t v = a.m > kFloor ? order_of(a.m) : 0u;
+        if (groups_all == 0) {
+          v = __shfl_sync(0xffffffffu, sort32(v, lane), 32 - K);
+        } else if (K <= kFewTops || kThreads == kFew) {
+          // the same of the maxima of 32 groups of threads, in fewer steps. The first time all groups
+          // are waited for; later their maxima are taken as they are, since an older maximum of a
+          // group is an element as well.
+          constexpr int kWidth = kThreads / 32;
+#pragma unroll
+          for (int o = 1; o < kWidth; o *= 2) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+          volatile uint32_t* const groups = tops[0];
+          if ((lane & (kWidth - 1)) == 0) groups[threadIdx.x / kWidth] = v;
+          if (round == 0)
+            __syncthreads();
+          else
+            __syncwarp();
+          uint32_t x = groups[lane];
+          if (K <= kFewTops) {
+            for (int k = 0; k < K; ++k) {  // (equal maxima count as one)
+              v = __reduce_max_sync(0xffffffffu, x);
+              x = x == v ? 0u : x;
+            }
+          } else {  // the least of those with fewer than K above
+            int over = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) over += __shfl_sync(0xffffffffu, x, i) > x ? 1 : 0;
+            v = __reduce_min_sync(0xffffffffu, over < K ? x : 0xFFFFFFFFu);
+          }
+        } else {
+          v = sort32(v, lane);
           __syncthreads();
-          if (warp < o) tops[warp][lane] = merge32(tops[warp][lane], tops[warp + o][31 - lane], lane);
+          tops[warp][31 - lane] = v;
+          for (int o = kWarps / 2; o > 0; o >>= 1) {
+            __syncthreads();
+            if (warp < o) tops[warp][lane] = merge32(tops[warp][lane], tops[warp + o][31 - lane], lane);
+          }
+          __syncthreads();
+          v = tops[0][K - 1];
         }
-        __syncthreads();
-        const float b = below(value_of(tops[0][K - 1]));
-        if (!(b <= above)) above = b;
+        const float b = below(value_of(v));
+        if (b == b && !(b <= above)) above = b;
       }
       // the row's first elements come last here: of equal values they are the earlier ones
       if (round == mine) above = below(above);
     }
-    const bool last = round + 1 == rounds;
-    if (__any_sync(0xffffffffu, around || !(mx <= above)) || (last && count > 0)) {
-      uint32_t us = last && count > 0 ? 1u << (kU - 1) : 0u, lists_us = 0;  // vectors to look at, for the list
+    if (__any_sync(0xffffffffu, around || !(mx <= above))) {
+      uint32_t lists_us = 0;  // vectors to look at, for the list
 #pragma unroll
       for (int u = 0; u < kU; ++u) lists_us |= __any_sync(0xffffffffu, !(mu[u] <= above)) ? 1u << u : 0u;
-      us |= lists_us | (__any_sync(0xffffffffu, around) ? (1u << kU) - 1 : 0u);
+      uint32_t us = lists_us | (__any_sync(0xffffffffu, around) ? (1u << kU) - 1 : 0u);
 #pragma unroll 1
       while (us) {
         const int u = __ffs(us) - 1;
@@ -491,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
             earlier += __popc((more | same) & valid);
           }
         }
-        if (K > 0 && ((lists_us >> u & 1) || (!us && count > 0 && (last || (int)count >= K)))) {
+        if (K > 0 && (lists_us >> u & 1)) {
           uint32_t todo = 0;
           // The limit of before this vector, and equal values too: what a merge on the way brings
           // into the list may have a higher index than an equal value still to come.
@@ -499,64 +537,45 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
 #pragma unroll
           for (int i = 0; i < kN; ++i) todo |= !(E::get(v, i) <= from) ? 1u << i : 0u;
           todo &= valid;
-          // few candidates go into the list one by one, many by way of the buffer
-          const bool few = count == 0 && __reduce_add_sync(0xffffffffu, (uint32_t)__popc(todo)) <= 8;
-          for (;;) {
-            uint32_t who = __ballot_sync(0xffffffffu, todo != 0);
+          for (uint32_t who; (who = __ballot_sync(0xffffffffu, todo != 0)) != 0; todo &= todo - 1) {
             const int i = __ffs(todo) - 1;  // this lane's next candidate
-            float x = E::get(v, 0);
-#pragma unroll
-            for (int j = 1; j < kN; ++j) x = i == j ? E::get(v, j) : x;
-            const uint64_t key = key_of(x, (uint32_t)(e0 + i));
-            if (few) {
-              if (!who) break;
-              for (; who; who &= who - 1) {
-                const uint64_t k = __shfl_sync(0xffffffffu, key, __ffs(who) - 1);
-                if (k > least) {
-                  const int place = __popc(__ballot_sync(0xffffffffu, list > k));
-                  const uint64_t prev = __shfl_up_sync(0xffffffffu, list, 1);
-                  list = lane < place ? list : (lane == place ? k : prev);
-                  least = __shfl_sync(0xffffffffu, list, K - 1);
-                }
+            if (todo) buffers[warp][count + __popc(who & ((1u << lane) - 1))] = key_of(E::pick(v, i), (uint32_t)(e0 + i));
+            count += __popc(who);
+            if (count >= 32) {
+              __syncwarp();
+              const uint64_t k = buffers[warp][lane];
+              count -= 32;
+              const uint64_t left = (uint32_t)lane < count ? buffers[warp][lane + 32] : 0;  // never beyond 63
+              __syncwarp();
+              buffers[warp][lane] = left;
+              list = merge32(list, sort32(k, lane), lane);
+              const uint64_t least = __shfl_sync(0xffffffffu, list, K - 1);
+              if (least != 0) {
+                const float own = value_of((uint32_t)(least >> 32));
+                if (!(own <= above)) above = own;
               }
-            } else {
-              if (todo) buffers[warp][count + __popc(who & ((1u << lane) - 1))] = key;
-              count += __popc(who);
-              // a list's worth at a group's end: the limit it brings spares the next groups this path
-              const bool rest = !who && !us && count > 0 && ((int)count >= K || last);
-              if (count >= 32 || rest) {
-                __syncwarp();
-                const uint32_t here = min(count, 32u);  // the buffer is never beyond 63
-                const uint64_t k = (uint32_t)lane < here ? buffers[warp][lane] : 0;
-                const uint64_t left = (uint32_t)lane + 32 < count ? buffers[warp][lane + 32] : 0;
-                __syncwarp();
-                buffers[warp][lane] = left;
-                count -= here;
-                list = merge32(list, sort32(k, lane), lane);
-                least = __shfl_sync(0xffffffffu, list, K - 1);
-                __syncwarp();
-              }
-              if (!who && !(rest && count > 0)) break;
+              __syncwarp();
             }
-            todo &= todo - 1;
           }
-          if (least != 0) {
-            const float own = value_of((uint32_t)(least >> 32));
-            if (!(own <= above)) above = own;
-                }
         }
       }
     }
   }
-  if (K > 0) lists[warp][lane] = list;
-  auto join_lanes = [&](int lanes) {  // the sums and counts of the first `lanes` lanes, in every lane
+  __syncwarp();
+  // this lane's key of those still in the buffer (31 at most); their number, and 65536 if the warp has a list
+  const uint64_t kept = (uint32_t)lane < count ? buffers[warp][lane] : 0;
+  if (K > 0 && lane == 0) pending[warp] = count | (list != 0 ? 1u << 16 : 0u);
+  // The sums and counts of the first `lanes` lanes (the others repeat them), in every lane: at the
+  // greatest point of reference, so that one rescaling serves all.
+  auto join_lanes = [&](int lanes) {
+    const float m = value_of(__reduce_max_sync(0xffffffffu, order_of(a.m)));
+    const float d = max_nan(point(a.m) - point(m), kFar), c = exp2_fast(d);
+    a.t = c * (a.t + d * a.s);
+    a.s = c * a.s;
+    a.m = m;
     for (int o = lanes / 2; o > 0; o >>= 1) {
-      Sums b;
-      b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-      b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-      b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
-      // the same order on both sides of the exchange, so that all lanes agree in every bit
-      a = lane & o ? join(b, a) : join(a, b);
+      a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+      a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
       earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
     }
   };
@@ -577,7 +596,22 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
     before[warp] = earlier;
   }
   __syncthreads();
-  if (K > 0) merge_lists(kWarps);
+  if (K > 0) {
+    // the warps' remaining keys, in a row, and 32 at a time into the lists
+    uint64_t* const pool = &buffers[0][0];
+    const uint32_t theirs = lane < kWarps ? pending[lane] : 0;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, theirs), keys = all & 0xFFFFu;
+    const uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? theirs & 0xFFFFu : 0u);
+    if ((uint32_t)lane < count) pool[at + lane] = kept;
+    __syncthreads();
+    for (uint32_t c = warp * 32; c < keys; c += kWarps * 32)
+      list = merge32(list, sort32(c + lane < keys ? pool[c + lane] : 0, lane), lane);
+    lists[warp][lane] = list;
+    int n = kWarps;  // lists that hold anything
+    if (all < 1u << 16)
+      while (n > 1 && (uint32_t)(n / 2) * 32 >= keys) n /= 2;
+    merge_lists(n);
+  }
   if (warp == 0) {
     const int w = lane % kWarps;
     a = Sums{sums[w][0], sums[w][1], sums[w][2]};
@@ -712,7 +746,11 @@ int launch_rows(const LogprobArgs& a, cudaStream_t stream) {
   // give every SM its CTAs
   const int64_t groups = a.vocab / Elem<DT>::kN / 128, sms = device_sm_count();
   const bool few = a.rows * 16 <= sms && groups >= 8 * (kFew / 32) / 2;
-  if (groups < 32 && a.rows >= 8 * sms) return launch<DT, kShort>(a, 1, stream);
+  // Many rows: with small CTAs fewer warps wait at a row's start and end, with large ones the last
+  // wave is shorter and the lists' limits come from more threads. Measured with 128 / 256 threads
+  // (us): 4096 rows of 32000 with 5 alternatives 89 / 107, of 5001 38 / 65, 2047 of 152064 without
+  // a list 99 / 111, with 32 217 / 212; 1024 fp32 rows of 152064 with 5 135 / 122.
+  if ((groups < 32 || a.topk == 0) && a.rows >= 8 * sms) return launch<DT, kShort>(a, 1, stream);
   const int64_t warps = (few ? kFew : kMany) / 32, slots = few ? sms : 768 / kMany * sms;
   int ctas = 1;
   static_assert(kMany / 32 >= kMaxCtas && kFew / 32 >= kMaxCtas, "a warp takes the list of each CTA of a cluster");
