@@ -29,10 +29,11 @@
 // (inserted one by one: 117). One fp32 row of 152064 with 20 takes 13 us, most of it the latency of
 // the steps at its end (7.5 without the list).
 //
-// Masked entries: -inf is replaced by a value so low that its exponential is 0 (kFloor), which
-// keeps (z - M) exp(z - M) at 0 instead of NaN. A row whose maximum is not above that value (all
-// entries masked, or masks of the type's lowest value only) or is beyond +1e38 is summed
-// again with every difference clamped.
+// Masked entries: -inf, and what is below -2^26, is replaced by that value (kFloor), whose exponential
+// is 0 next to any maximum from -2^24 on; (z - M) exp(z - M) stays 0 instead of NaN. M log2 e is
+// rounded, by up to 1 at 2^24: the exponentials are off by that power of two, which ln S takes back.
+// A row whose maximum is of a greater magnitude (all entries masked, too) is summed again with exact
+// and clamped differences.
 #include <cstdint>
 #include <algorithm>
 #include <atomic>
@@ -52,7 +53,8 @@ constexpr int kU = 4;         // vectors of a lane in a group
 constexpr int kFewTops = 8;   // up to here a limit comes from 32 maxima
 constexpr int kShort = 128, kMany = 256, kFew = 1024;  // threads of a CTA: many short rows, many rows, few rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kFloor = -0x1.2cp126f;  // stands for -inf (0xFE96 in bf16): (kFloor - M) log2 e is finite, its exponential 0
+constexpr float kFloor = -0x1p26f;  // stands for -inf and all below it (0xCC80 in bf16)
+constexpr float kFarMax = 0x1p24f;  // a greater magnitude of the row's maximum takes a second pass
 constexpr float kFar = -1e30f;    // least difference of two maxima: times a sum it stays finite
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -163,7 +165,7 @@ struct Elem<FI_DTYPE_BF16> {
     return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
   // kFloor in bf16
-  __device__ static uint32_t lift(uint32_t w) { return max_bf16x2(w, 0xFE96FE96u); }
+  __device__ static uint32_t lift(uint32_t w) { return max_bf16x2(w, 0xCC80CC80u); }
   __device__ static uint32_t spread(float x) { return f32x2_to_bf16x2(x, x); }
   __device__ static uint32_t before(float x) {
     const uint32_t b = below16((uint16_t)f32_to_bf16_rn(x), 0xFF80u);
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   }
   __syncthreads();
   a = Sums{cta.m, cta.s, cta.t};
-  const bool far = a.m <= kFloor || a.m > 1e38f;
+  const bool far = !(fabsf(a.m) <= kFarMax);
   if (far) {
     // rare: the true maximum first, then sums with clamped differences, by this CTA alone
     float mx = __uint_as_float(0xFF800000u);

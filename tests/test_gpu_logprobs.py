@@ -152,6 +152,24 @@ def test_masked_rows(dtype, vocab):
     _check(z.to(dtype).cuda(), torch.full((12,), 14).cuda(), 4)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [300, 50001])
+def test_great_magnitudes(dtype, vocab):
+    """Logits of any magnitude: where one step of fp32 is more than the exponential's range, and masks
+    of finite values (whole threads, or rows, of nothing else)."""
+    sizes = [1e5, 1e7, 2e7, 6e7, 7e7, 1e9, 1e10, 1e12, 1e20, 1e30, 1e37]
+    z = torch.cat([_logits(len(sizes), vocab, torch.float32, 8) * torch.tensor(sizes)[:, None],
+                   _logits(len(sizes), vocab, torch.float32, 9), _logits(len(sizes), vocab, torch.float32, 10),
+                   -torch.tensor(sizes)[:, None] + _logits(len(sizes), vocab, torch.float32, 11)])
+    for i, size in enumerate(sizes):
+        z[len(sizes) + i, 20:] = -size          # one row's masks
+        z[2 * len(sizes) + i, :-20] = -size
+        z[2 * len(sizes) + i, -10:] = -INF
+    tokens = torch.arange(len(z)) * 5 % vocab
+    _check(z.to(dtype).cuda(), tokens.cuda(), 9)
+    _check(z.to(dtype).cuda(), z.argmax(1).cuda(), 0)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("vocab", [300, 50001])
 def test_nan_and_infinite_rows(dtype, vocab):
