@@ -1,7 +1,8 @@
 """bf16 activations x NVFP4 weights (mm_bf16_fp4) for NVIDIA B200 (sm_100a).
 
-A thin ctypes binding over the C-ABI library ``libfi_nvfp4.so`` (declared in
-``include/fi_nvfp4.h``). This module only marshals arguments: every step of the
+A thin binding over the C-ABI library ``libfi_nvfp4.so`` (declared in ``include/fi_nvfp4.h``):
+ctypes, and for the calls that a decode step makes in microseconds the native module ``_binding``.
+This module only marshals arguments: every step of the
 computation runs in the library's CUDA kernels. torch supplies device memory and the
 current CUDA stream. There is no CPU fallback: if the library is missing, every call
 raises.
@@ -367,54 +368,55 @@ def splitk_reduce(partials: torch.Tensor, gscale: torch.Tensor, out: torch.Tenso
 # --------------------------------------------- 8-bit products, a scale per block of 128
 
 # A decode call's kernel takes a few microseconds, so these functions are written for few host
-# microseconds: the quick checks first and the messages only where one fails, the raw stream handle
-# (a Stream object costs 2 us), outputs by empty_strided (0.5 us less than new_empty).
+# microseconds: the native module (csrc/binding.cpp) checks the arguments, makes the outputs and calls
+# the library in one step, and answers None to arguments that it does not take. They go through the
+# checks here, which say what is wrong.
 
-def _call(name: str, device: int, *args) -> None:
-    """library().name(*args, current stream of `device`), with that device current."""
-    fn = getattr(_lib or library(), name)
-    stream = torch._C._cuda_getCurrentRawStream(device)
-    if device == torch._C._cuda_getDevice():
-        st = fn(*args, stream)
-    else:  # the library works on the current device
-        with torch.cuda.device(device):
-            st = fn(*args, stream)
-    if st:
-        _check(st, name)
+_native = None
 
 
-def _is(t, dtype: torch.dtype, ndim: int) -> bool:
-    """What _require asks, without its message."""
-    return isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+def _load_binding():
+    """The native module, bound to the loaded library (both are built together)."""
+    global _native
+    lib = library()
+    with _lock:
+        if _native is None:
+            path = os.path.join(_HERE, "_binding.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it with `python -m bf16_activations_nvfp4_b200.build` "
+                                   "(there is no fallback implementation)")
+            from . import _binding
+            _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.fi_fp8_quantize, lib.fi_fp8_pack_weights, lib.fi_mm_fp8, lib.fi_mm_fp8_gated,
+                lib.fi_token_logprobs)))
+            _native = _binding
+    return _native
 
 
-def _empty(rows: int, columns: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
-    return torch.empty_strided((rows, columns), (max(columns, 1), 1), dtype=dtype, device=device)
+def _done(r, where: str):
+    """What the native module returned, or the error that its status stands for."""
+    if type(r) is int:
+        _check(r, where)
+    return r
 
 
 def _quantize(where: str, x: torch.Tensor, name: str, square: bool, out: tuple | None):
-    code = _DTYPES_ANY.get(x.dtype) if isinstance(x, torch.Tensor) else None
-    if code is None:
+    if out is not None and (len(out) != 2 or out[0] is None):
+        raise ValueError("out must be (codes, scale)")
+    q, s = out or (None, None)
+    r = (_native or _load_binding()).quantize(x, square, q, s)
+    if r is not None:
+        return _done(r, where)
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES_ANY:
         raise ValueError(f"{name} must be a bf16, f16 or fp32 tensor")
-    if not (x.is_cuda and x.dim() == 2 and x.is_contiguous()):
-        _require(x, name, x.dtype, 2)
+    _require(x, name, x.dtype, 2)
     rows, k = x.shape
     tall, wide = -(-rows // FP8_BLOCK) if square else rows, -(-k // FP8_BLOCK)
-    if out is None:
-        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        s = _empty(tall, wide, torch.float32, x.device)
-    else:
-        if len(out) != 2:
-            raise ValueError("out must be (codes, scale)")
-        q, s = out
-        _require(q, "codes", torch.float8_e4m3fn, 2)
-        _require(s, "scale", torch.float32, 2)
-        if q.shape != (rows, k) or s.shape != (tall, wide):
-            raise ValueError(f"codes must be [{rows}, {k}] and scale [{tall}, {wide}], got {list(q.shape)} and "
-                             f"{list(s.shape)}")
-        _same_device(x, codes=q, scale=s)
-    _call(where, x.get_device(), x.data_ptr(), code, rows, k, q.data_ptr(), s.data_ptr())
-    return q, s
+    _require(q, "codes", torch.float8_e4m3fn, 2)
+    _require(s, "scale", torch.float32, 2)
+    _same_device(x, codes=q, scale=s)
+    raise ValueError(f"codes must be [{rows}, {k}] and scale [{tall}, {wide}], got {list(q.shape)} and "
+                     f"{list(s.shape)}")
 
 
 def quantize_fp8(A: torch.Tensor, out: tuple | None = None):
@@ -432,9 +434,8 @@ def pack_weights_fp8(W: torch.Tensor, out: tuple | None = None):
 
 def _fp8_operand(q: torch.Tensor, s: torch.Tensor, k: int | None, rows: int, qn: str, sn: str) -> tuple:
     """(rows, k) of a matrix of codes [r, k] and its scales, one per `rows` rows and block of k."""
-    if not (_is(q, torch.float8_e4m3fn, 2) and _is(s, torch.float32, 2)):
-        _require(q, qn, torch.float8_e4m3fn, 2)
-        _require(s, sn, torch.float32, 2)
+    _require(q, qn, torch.float8_e4m3fn, 2)
+    _require(s, sn, torch.float32, 2)
     r, kq = q.shape
     sr, sk = s.shape
     if (k is not None and kq != k) or sr != -(-r // rows) or sk != -(-kq // FP8_BLOCK):
@@ -443,18 +444,25 @@ def _fp8_operand(q: torch.Tensor, s: torch.Tensor, k: int | None, rows: int, qn:
     return r, kq
 
 
-def _fp8_out(Aq: torch.Tensor, m: int, n: int, out: torch.Tensor | None, out_dtype: torch.dtype | None):
+def _refuse_product(Aq: torch.Tensor, Ascale: torch.Tensor, weights: dict, out: torch.Tensor | None,
+                    out_dtype: torch.dtype | None):
+    """Raises what is wrong with a product's arguments; `weights` are its codes and scales by name."""
+    m, k = _fp8_operand(Aq, Ascale, None, 1, "Aq", "Ascale")
+    n = None
+    for name in [w for w in weights if w.endswith("q")]:
+        scale = name[0] + "scale"
+        r, _ = _fp8_operand(weights[name], weights[scale], k, FP8_BLOCK, name, scale)
+        if n is not None and r != n:
+            raise ValueError(f"Gq has {n} rows and {name} {r}")
+        n = r
+    _same_device(Aq, Ascale=Ascale, **weights)
     dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
     if dtype not in _DTYPES_ANY or (out_dtype is not None and out_dtype != dtype):
         raise ValueError(f"the output is bf16, f16 or fp32 (out_dtype {out_dtype}, out "
                          f"{None if out is None else out.dtype})")
-    if out is None:
-        return _empty(m, n, dtype, Aq.device), dtype
     _require(out, "out", dtype, 2)
-    if out.shape != (m, n):
-        raise ValueError(f"out must be [{m}, {n}], got {tuple(out.shape)}")
     _same_device(Aq, out=out)
-    return out, dtype
+    raise ValueError(f"out must be [{m}, {n}], got {tuple(out.shape)}")
 
 
 def mm_fp8(Aq: torch.Tensor, Ascale: torch.Tensor, Wq: torch.Tensor, Wscale: torch.Tensor,
@@ -462,15 +470,10 @@ def mm_fp8(Aq: torch.Tensor, Ascale: torch.Tensor, Wq: torch.Tensor, Wscale: tor
     """out[m, n] = (Aq scaled by Ascale) . (Wq scaled by Wscale)^T for codes and scales of
     quantize_fp8 and pack_weights_fp8; fp32 sums, bf16 out unless out_dtype (or the dtype of
     `out`) is torch.float16 or torch.float32. Any m; k a multiple of 16."""
-    m, k = _fp8_operand(Aq, Ascale, None, 1, "Aq", "Ascale")
-    n, _ = _fp8_operand(Wq, Wscale, k, FP8_BLOCK, "Wq", "Wscale")
-    dev = Aq.get_device()
-    if Ascale.get_device() != dev or Wq.get_device() != dev or Wscale.get_device() != dev:
-        _same_device(Aq, Ascale=Ascale, Wq=Wq, Wscale=Wscale)
-    out, dtype = _fp8_out(Aq, m, n, out, out_dtype)
-    _call("fi_mm_fp8", dev, Aq.data_ptr(), Ascale.data_ptr(), Wq.data_ptr(), Wscale.data_ptr(), out.data_ptr(),
-          _DTYPES_ANY[dtype], m, n, k)
-    return out
+    r = (_native or _load_binding()).mm(Aq, Ascale, Wq, Wscale, out, out_dtype)
+    if r is None:
+        _refuse_product(Aq, Ascale, {"Wq": Wq, "Wscale": Wscale}, out, out_dtype)
+    return _done(r, "fi_mm_fp8")
 
 
 def mm_fp8_gated(Aq: torch.Tensor, Ascale: torch.Tensor, Gq: torch.Tensor, Gscale: torch.Tensor,
@@ -479,18 +482,10 @@ def mm_fp8_gated(Aq: torch.Tensor, Ascale: torch.Tensor, Gq: torch.Tensor, Gscal
     """silu(A G^T) * (A U^T) [m, n] in one kernel, both products as mm_fp8 computes them and not
     rounded before the activation. G and U are [n, k]; of a fused [2n, k] weight with n a multiple
     of 128, pass the two halves of its codes and scales."""
-    m, k = _fp8_operand(Aq, Ascale, None, 1, "Aq", "Ascale")
-    n, _ = _fp8_operand(Gq, Gscale, k, FP8_BLOCK, "Gq", "Gscale")
-    if _fp8_operand(Uq, Uscale, k, FP8_BLOCK, "Uq", "Uscale")[0] != n:
-        raise ValueError(f"Gq has {n} rows and Uq {Uq.shape[0]}")
-    dev = Aq.get_device()
-    for t in (Ascale, Gq, Gscale, Uq, Uscale):
-        if t.get_device() != dev:
-            _same_device(Aq, Ascale=Ascale, Gq=Gq, Gscale=Gscale, Uq=Uq, Uscale=Uscale)
-    out, dtype = _fp8_out(Aq, m, n, out, out_dtype)
-    _call("fi_mm_fp8_gated", dev, Aq.data_ptr(), Ascale.data_ptr(), Gq.data_ptr(), Gscale.data_ptr(), Uq.data_ptr(),
-          Uscale.data_ptr(), out.data_ptr(), _DTYPES_ANY[dtype], m, n, k)
-    return out
+    r = (_native or _load_binding()).gated(Aq, Ascale, Gq, Gscale, Uq, Uscale, out, out_dtype)
+    if r is None:
+        _refuse_product(Aq, Ascale, {"Gq": Gq, "Gscale": Gscale, "Uq": Uq, "Uscale": Uscale}, out, out_dtype)
+    return _done(r, "fi_mm_fp8_gated")
 
 
 class TokenLogprobs(NamedTuple):
@@ -506,30 +501,20 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, topk: int = 0) ->
     one token per row: logits [rows, vocab] (bf16, f16 or fp32; rows may be further apart than
     vocab, as in a padded lm_head), tokens int64 [rows]. Equal logits order by index; -inf entries
     are masked; a token outside the vocabulary has logprob NaN and rank -1."""
+    r = (_native or _load_binding()).logprobs(logits, tokens, topk)
+    if type(r) is tuple:
+        return tuple.__new__(TokenLogprobs, r)
+    if r is not None:
+        _check(r, "fi_token_logprobs")
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in _DTYPES_ANY or logits.dim() != 2:
         raise ValueError("logits must be a 2-d bf16, f16 or fp32 CUDA tensor")
-    if not _is(tokens, torch.int64, 1):
-        _require(tokens, "tokens", torch.int64, 1)
-    rows, vocab = logits.shape
-    ld, inner = logits.stride()
-    if rows <= 1:
-        ld = vocab
-    if (vocab > 1 and inner != 1) or ld < vocab:
-        raise ValueError("the logits of a row must be adjacent and the rows must not overlap")
-    if tokens.shape[0] != rows:
-        raise ValueError(f"tokens must be [{rows}], got {tuple(tokens.shape)}")
-    dev = logits.get_device()
-    if tokens.get_device() != dev:
-        _same_device(logits, tokens=tokens)
-    kk = max(0, min(topk, vocab))
-    rank = torch.empty_like(tokens)
-    lp = torch.empty_like(tokens, dtype=torch.float32)
-    ent = torch.empty_like(lp)
-    top = _empty(rows, kk, torch.float32, logits.device)
-    ids = torch.empty_like(top, dtype=torch.int64)
-    _call("fi_token_logprobs", dev, logits.data_ptr(), _DTYPES_ANY[logits.dtype], rows, vocab, ld, tokens.data_ptr(),
-          topk, lp.data_ptr(), ent.data_ptr(), rank.data_ptr(), top.data_ptr(), ids.data_ptr())
-    return TokenLogprobs(lp, ent, rank, top, ids)
+    _require(tokens, "tokens", torch.int64, 1)
+    if tokens.shape[0] != logits.shape[0]:
+        raise ValueError(f"tokens must be [{logits.shape[0]}], got {tuple(tokens.shape)}")
+    _same_device(logits, tokens=tokens)
+    if not isinstance(topk, int):
+        raise TypeError(f"topk must be an int, got {type(topk).__name__}")
+    raise ValueError("the logits of a row must be adjacent and the rows must not overlap")
 
 
 def lm_head_logprobs(A: torch.Tensor, weight: tuple, tokens: torch.Tensor, topk: int = 0) -> TokenLogprobs:

@@ -1,10 +1,11 @@
-"""Build libfi_nvfp4.so in-tree with nvcc for sm_100a (B200).
+"""Build libfi_nvfp4.so in-tree with nvcc for sm_100a (B200), and the Python module _binding.so.
 
     python -m bf16_activations_nvfp4_b200.build [--force]
 
 Each csrc/*.cu is compiled to an object under _build/ (skipped when up to date), then
 linked into bf16_activations_nvfp4_b200/libfi_nvfp4.so with the CUDA runtime linked
-statically, so the library loads without a CUDA install path and without a GPU.
+statically, so the library loads without a CUDA install path and without a GPU. csrc/binding.cpp
+is compiled by the host compiler against the installed torch.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfi_nvfp4.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -47,6 +50,20 @@ def _stale(target: str, sources: list[str]) -> bool:
     return any(os.path.getmtime(s) > t for s in sources)
 
 
+def _binding_command(nvcc: str, target: str) -> list[str]:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    paths = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
+    # torch's libraries are in the process before the module is: no run path
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-isystem" + p for p in paths],
+            os.path.join(CSRC, "binding.cpp"), "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch_python", "-o", target]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -59,18 +76,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + deps + [__file__]):
             jobs.append([nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj])
+    link = force or bool(jobs)
+    binding_tmp = BINDING + f".tmp{os.getpid()}"
+    binding_sources = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "fi_nvfp4.h"), __file__]
+    binding = force or _stale(BINDING, binding_sources)
+    if binding:
+        jobs.append(_binding_command(nvcc, binding_tmp))
 
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {cmd[-3]}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-3]}:\n{r.stdout}\n{r.stderr}")
         return r
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
+    if binding:
+        os.replace(binding_tmp, BINDING)
+    if link or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)

@@ -102,3 +102,15 @@ def test_binding_refuses_host_tensors_and_wrong_types():
                  lambda: fi.token_logprobs(x, torch.zeros(4, dtype=torch.int64))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_says_what_is_wrong():
+    """The native module takes none of these; the message names the argument."""
+    q, s = torch.zeros((4, 64), dtype=torch.float8_e4m3fn), torch.zeros((4, 1))
+    for call, word in ((lambda: fi.quantize_fp8(torch.zeros((4, 64)), out=(q,)), "codes, scale"),
+                       (lambda: fi.quantize_fp8(torch.zeros((4, 64)), out=(None, None)), "codes, scale"),
+                       (lambda: fi.quantize_fp8(None), "A must be"), (lambda: fi.pack_weights_fp8(q), "W must be"),
+                       (lambda: fi.mm_fp8(q, s, q, s), "Aq must be"), (lambda: fi.mm_fp8(None, s, q, s), "Aq must be"),
+                       (lambda: fi.token_logprobs(None, None), "logits must be")):
+        with pytest.raises(ValueError, match=word):
+            call()
