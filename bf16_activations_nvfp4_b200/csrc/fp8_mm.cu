@@ -43,7 +43,7 @@ constexpr int kTileRows = 128;                     // weight rows per tile (the 
 constexpr uint32_t kTileBytes = kTileRows * 128;   // a tile of one k block
 constexpr int kGroup = 4, kGroups = 2;             // blocks of k whose scales share a barrier; groups in the ring
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi0 = 3;
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 10, kMaxBufs = 4;
 constexpr int kMaxSplits = 8;                      // CTAs of a portable cluster
 
 // The geometry of one instance: N activation rows per tile, one weight tile or two (gated).
@@ -56,16 +56,20 @@ struct Geo {
   static constexpr uint32_t kStageBytes = kTiles * kTileBytes + N * 128;
   static constexpr int kCtas = (GATED ? N <= 32 : N <= 96) ? 2 : 1;  // resident per SM
   static constexpr int kTmemCols = 512 / kCtas < kTiles * N * 4 ? 512 / kCtas : kTiles * N * 4;
-  static constexpr int kBufs = kTmemCols / (kTiles * N);  // blocks the tensor core may be ahead
   static constexpr uint32_t kBudget = kCtas == 2 ? 112 * 1024 : 226 * 1024;
   static constexpr uint32_t kScaleBytes = kGroups * kGroup * kTiles * N * 4;
-  static constexpr uint32_t kFixed = 1024 + kScaleBytes + (2 * kMaxStages + kBufs + 2 * kGroups + 1) * 8 + 64;
+  static constexpr uint32_t kFixed = 1024 + kScaleBytes + (2 * kMaxStages + kMaxBufs + 2 * kGroups + 1) * 8 + 64;
   static constexpr int kStages =
       (kBudget - kFixed) / kStageBytes < kMaxStages ? (kBudget - kFixed) / kStageBytes : kMaxStages;
+  // Blocks the tensor core may be ahead of the epilogue: not more than there are stages, since a
+  // stage's barrier tells the epilogue of its block, too, by one bit of its phase; twice on, it would read as not
+  // there yet.
+  static constexpr int kTmemBufs = kTmemCols / (kTiles * N);
+  static constexpr int kBufs = kTmemBufs < kStages ? kTmemBufs : kStages;
   static constexpr uint32_t kRing = kStages * kStageBytes;
   static constexpr uint32_t kSmem = kFixed + kRing;
   static_assert(kStages >= 3, "ring");
-  static_assert(kBufs >= 2 && kBufs * kTiles * N <= 512, "TMEM");
+  static_assert(kBufs >= 2 && kBufs <= kStages && kBufs <= kMaxBufs && kBufs * kTiles * N <= kTmemCols, "TMEM");
   static_assert((uint32_t)(kTiles * N) * kTileRows * 4 <= kRing, "the split sums reuse the ring");
 };
 

@@ -46,6 +46,7 @@ constexpr uint32_t kScaleBytes = kGroups * kGroup * 2 * kRows * 4;
 constexpr uint32_t kBarBytes = (2 * kStages + kBufs + 2 * kGroups + 1) * 8;
 constexpr int kGroupM = 8;  // 4, 12, 16 and 32 are within 3%
 constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kOutBytes + kScaleBytes + kBarBytes;
+static_assert(kBufs <= kStages, "an epilogue that is behind sees each block's barrier before its next phase is over");
 static_assert(32 * 128 <= kOutBytes / 8, "a warp stages 128 bytes of 32 rows");
 constexpr int kEpiRegs = 216, kOtherRegs = 64;
 // registers after the split: the epilogue's two warpgroups and the other one stay within the launch's 168 a thread

@@ -380,3 +380,21 @@ print("captured")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("m", [1, 16, 17, 32, 64])
+@pytest.mark.parametrize("n,k", [(40000, 2048), (4096, 4096), (1000, 14336)])
+def test_gated_waves_one_after_another(m, n, k):
+    """Many CTAs, two on an SM, and calls that follow one another without a pause: an epilogue that falls
+    behind its tensor core still sees every block."""
+    a = fi.quantize_fp8(torch.randn((m, k), generator=torch.Generator().manual_seed(m)).cuda())
+    w = fi.pack_weights_fp8(torch.randn((n, k), generator=torch.Generator().manual_seed(n)).cuda())
+    ref = fi.mm_fp8_gated(*a, *w, *w, out_dtype=torch.float32)
+    g = fi.mm_fp8(*a, *w, out_dtype=torch.float32).double()
+    # the two calls add the same blocks in fp32, in another order of K splits
+    tol = 2.0 ** -16 * (g.abs().amax() ** 2 + 1)
+    assert ((ref.double() - g * torch.sigmoid(g) * g).abs() <= tol).all()
+    got = [fi.mm_fp8_gated(*a, *w, *w, out_dtype=torch.float32) for _ in range(40)]
+    torch.cuda.synchronize()
+    assert fi.get_device_error() == 0
+    assert all(torch.equal(x, ref) for x in got)
