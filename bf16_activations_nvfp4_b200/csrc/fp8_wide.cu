@@ -166,28 +166,37 @@ __device__ __forceinline__ void store_rows(const Fp8MmArgs& p, bool wide, const 
                    : "memory");
     }
     __syncwarp();
-    const int64_t col = col0 + c + (lane % 8) * per;
-    uint8_t* dst = static_cast<uint8_t*>(p.out) + (row0 + lane / 8) * pitch + col * es;
-    const bool whole = wide && row0 + 32 <= p.m && col0 + c + kStep <= p.n;
+    if (wide && row0 + 32 <= p.m && col0 + c + kStep <= p.n) {
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + (row0 + lane / 8) * pitch + (col0 + c + (lane % 8) * per) * es;
 #pragma unroll 1
-    for (int r = lane / 8; r < 32; r += 4) {
-      uint4 v;
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(piece(r, lane % 8)));
-      if (whole) {
+      for (int r = lane / 8; r < 32; r += 4) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(piece(r, lane % 8)));
         *reinterpret_cast<uint4*>(dst) = v;
-      } else if (row0 + r < p.m) {
-#pragma unroll 1
-        for (int e = 0; e < per && col + e < p.n; ++e) {
-          const uint32_t word = e * es < 8 ? (e * es < 4 ? v.x : v.y) : (e * es < 12 ? v.z : v.w);
-          if (es == 4)
-            reinterpret_cast<uint32_t*>(dst)[e] = word;
-          else
-            reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(e & 1 ? word >> 16 : word);
-        }
+        dst += 4 * pitch;
       }
-      dst += 4 * pitch;
+    } else {
+      // rows of any pitch: a row's 128 bytes by all lanes, a word each, so that neighbouring lanes
+      // write neighbouring addresses. A word whose address is odd to it goes as two halves. (Element by
+      // element in the order above: 339 x 12610 x 2480 to f16 52 us.)
+      const int rows = (int)min((int64_t)32, p.m - row0);
+      const int64_t col = col0 + c + lane * (4 / es);
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + row0 * pitch + col * es;
+      const bool words = es == 4 || (p.n % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0);
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(piece(r, lane / 4) + (uint32_t)(lane % 4) * 4));
+        if (words) {
+          if (col < p.n) *reinterpret_cast<uint32_t*>(dst) = v;
+        } else {
+          if (col < p.n) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)v;
+          if (col + 1 < p.n) *reinterpret_cast<uint16_t*>(dst + 2) = (uint16_t)(v >> 16);
+        }
+        dst += pitch;
+      }
     }
     __syncwarp();
   }
