@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
 // Launched never: stands for the kernels' shape in the occupancy query.
 __global__ void shape_kernel() {}
 
-// How a call is cut, and what it is expected to take in tenths of a block of the CTA-pair kernel
-// (a block of 128 k of one tile there takes about 0.36 us).
+// How a call is cut, and what it is expected to take, in tenths of a block of the CTA-pair kernel (a
+// block of 128 k of one tile there takes about 0.36 us).
 struct Cut {
   int splits;
   int64_t units;  // tiles of weight rows x tiles of activation rows
@@ -353,8 +353,10 @@ struct Cut {
 
 // The split of least cost: waves of clusters, each with its blocks of k, a start and an end, and the
 // meeting of a cluster. Measured on B200: a block of N = 256 rows takes 0.72 us, one of the gated
-// N = 128 0.9 us, one of N = 128 0.32 us, one of N = 96 with two CTAs on every SM 0.65 us; a wave's
-// start and end 7 us.
+// N = 128 0.9 us, of the gated N = 64 0.4 us, one of N = 128 0.37 us, one of N = 96 with two CTAs on
+// every SM 0.65 us; a wave's start and end 5.2 us (the gated N = 64: 6.7) and 0.03 us per row that a CTA
+// writes (of the gated N = 128, whose splits have twice as much to read from one another, half of that and
+// 0.2 us a split); up to 96 rows a wave's start and end count as 7 us.
 template <int N, bool GATED>
 int cut_tiles(const Fp8MmArgs& a, Cut* out) {
   using G = Geo<N, GATED>;
@@ -392,13 +394,17 @@ int cut_tiles(const Fp8MmArgs& a, Cut* out) {
     }
     active[dev][0] = 1;
   }
-  constexpr int64_t kBlock = N == 256 ? 20 : (GATED && N == 128 ? 24 : (N == 96 ? 18 : 9));
+  constexpr bool kMid = N >= 128 || (GATED && N == 64);  // tiles that compete with one another
+  constexpr int64_t kBlock = N == 256 ? 20 : (GATED && N == 128 ? 24 : (N == 96 ? 18 : (GATED && N == 64 ? 11 : (N == 128 ? 10 : 9))));
+  constexpr int64_t kWave = !kMid ? 200 : (N == 64 ? 185 : 145);
+  const int64_t wrote = kMid ? std::min<int64_t>(a.m, N) * 8 / 10 : 0;
   out->units = (a.n + kTileRows - 1) / kTileRows * ((a.m + N - 1) / N);
   out->cost = -1;
   for (int s = 1; s <= kMaxSplits && s <= a.kblocks; ++s) {
     const int64_t at_once = active[dev][s];
     const int64_t cost =
-        (out->units + at_once - 1) / at_once * ((a.kblocks + s - 1) / s * kBlock + 200) + (s > 1 ? 40 : 0);
+        (out->units + at_once - 1) / at_once * ((a.kblocks + s - 1) / s * kBlock + kWave + (s > 1 && GATED && N == 128 ? wrote / 2 + 6 * s : wrote / s)) +
+        (s > 1 ? 40 : 0);
     if (out->cost < 0 || cost < out->cost) {
       out->cost = cost;
       out->splits = s;
@@ -440,33 +446,38 @@ int launch_tile(Fp8MmArgs a, const Cut& cut, cudaStream_t stream) {
   return FI_OK;
 }
 
-// This kernel, or the CTA-pair kernel where that is expected to take less: from the rows of a
-// whole tile on, when its tiles of 256 rows x 256 columns keep enough CTA pairs busy. Measured (us,
-// this kernel / CTA pairs): 256 rows of 34816 x 5120 78.5 / 49.9, of 4096 x 14336 28.7 / 49.1; 512
-// rows of 2048 x 7168 18.5 / 28.5, of 34816 x 5120 154 / 88.5.
-template <int N, bool GATED>
-int launch_cheapest(const Fp8MmArgs& a, cudaStream_t stream) {
-  Cut cut;
-  const int rc = cut_tiles<N, GATED>(a, &cut);
-  if (rc != FI_OK) return rc;
-  if (N == 256 || (GATED && N == 128)) {
-    const int64_t tiles = (a.m + 255) / 256 * ((a.n + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-    const int64_t pairs = std::max(1, device_sm_count() / 2);
-    if ((tiles + pairs - 1) / pairs * (a.kblocks * 10 + 150) + 90 < cut.cost) return launch_fp8_wide(a, GATED, stream);
-  }
-  return launch_tile<N, GATED>(a, cut, stream);
+// What the CTA-pair kernel is expected to take: 0.36 us a block (0.4 where one row of tiles reads
+// all weights and HBM counts), 4 us a wave and 2.5 us a call.
+int64_t wide_cost(const Fp8MmArgs& a, bool gated) {
+  const int64_t tiles_m = (a.m + 255) / 256, tiles = tiles_m * ((a.n + (gated ? 127 : 255)) / (gated ? 128 : 256));
+  const int64_t pairs = std::max(1, device_sm_count() / 2);
+  return (tiles + pairs - 1) / pairs * (a.kblocks * (gated && tiles_m == 1 ? 11 : 10) + 110) + 70;
 }
 
-// 65 to 96 rows: tiles of 96 rows two to an SM, or of 128 rows one to an SM, which take half as long
-// each. The first where there are enough tiles for both places: measured (us, 96 / 128) 77 rows of
-// 10304 x 2688 11.7 / 13.9, 80 of 34816 x 5120 37.3 / 43.3, 96 of 248320 x 5120 280 / 315; 96 of
-// 4096 x 4096 12.0 / 9.7, of 2048 x 7168 11.2 / 9.8.
-int launch_96(const Fp8MmArgs& a, cudaStream_t stream) {
-  Cut two, one;
-  int rc = cut_tiles<96, false>(a, &two);
-  if (rc == FI_OK) rc = cut_tiles<128, false>(a, &one);
+// The cheapest of two tiles of this kernel and, where `pair` says so, the CTA-pair kernel. Measured
+// (us):
+//   65 to 96 rows, tiles of 96 rows two to an SM / of 128 one to an SM: 77 of 10304 x 2688 11.7 / 13.9,
+//   80 of 34816 x 5120 37.3 / 43.3, 96 of 248320 x 5120 280 / 315, of 4096 x 4096 12.0 / 9.7;
+//   from 129 rows on, tiles of 128 / 256 / CTA pairs: 256 of 178 x 768 5.6 / 8.1 / 8.3, of 2048 x 7168
+//   12.0 / 15.4 / 25.6, 130 of 4096 x 14336 28.1 / 25.3 / 46.6, 391 of 4096 x 4096 20.9 / 20.5 / 17.7,
+//   256 of 5295 x 416 10.1 / 16.0 / 8.5, 1000 of 4096 x 4096 41.4 / 35.0 / 18.9;
+//   gated from 65 rows on, tiles of 64 / 128 / CTA pairs: 128 of 65 x 11408 11.5 / 18.1 / 38.3, of
+//   1746 x 1136 8.6 / 10.7 / 9.2, of 17408 x 5120 53.9 / 44.5 / 45.5, 200 of 8192 x 2048 30.3 / 24.6 / 13.2.
+template <int N1, int N2, bool GATED>
+int launch_cheapest(const Fp8MmArgs& a, bool pair, cudaStream_t stream) {
+  Cut one, two;
+  int rc = cut_tiles<N1, GATED>(a, &one);
+  if (rc == FI_OK) rc = cut_tiles<N2, GATED>(a, &two);
   if (rc != FI_OK) return rc;
-  return two.cost < one.cost ? launch_tile<96, false>(a, two, stream) : launch_tile<128, false>(a, one, stream);
+  if (pair && wide_cost(a, GATED) < std::min(one.cost, two.cost)) return launch_fp8_wide(a, GATED, stream);
+  return one.cost < two.cost ? launch_tile<N1, GATED>(a, one, stream) : launch_tile<N2, GATED>(a, two, stream);
+}
+
+template <int N, bool GATED>
+int launch_only(const Fp8MmArgs& a, cudaStream_t stream) {
+  Cut cut;
+  const int rc = cut_tiles<N, GATED>(a, &cut);
+  return rc != FI_OK ? rc : launch_tile<N, GATED>(a, cut, stream);
 }
 
 }  // namespace
@@ -477,17 +488,16 @@ int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream) {
   a.timeout_ns = wait_timeout_ns();
   a.debug_stall = take_debug_stall();
   if (gated) {
-    if (a.m <= 16) return launch_cheapest<16, true>(a, stream);
-    if (a.m <= 32) return launch_cheapest<32, true>(a, stream);
-    if (a.m <= 64) return launch_cheapest<64, true>(a, stream);
-    return launch_cheapest<128, true>(a, stream);
+    if (a.m <= 16) return launch_only<16, true>(a, stream);
+    if (a.m <= 32) return launch_only<32, true>(a, stream);
+    if (a.m <= 64) return launch_only<64, true>(a, stream);
+    return launch_cheapest<64, 128, true>(a, true, stream);
   }
-  if (a.m <= 16) return launch_cheapest<16, false>(a, stream);
-  if (a.m <= 32) return launch_cheapest<32, false>(a, stream);
-  if (a.m <= 64) return launch_cheapest<64, false>(a, stream);
-  if (a.m <= 96) return launch_96(a, stream);
-  if (a.m <= 128) return launch_cheapest<128, false>(a, stream);
-  return launch_cheapest<256, false>(a, stream);
+  if (a.m <= 16) return launch_only<16, false>(a, stream);
+  if (a.m <= 32) return launch_only<32, false>(a, stream);
+  if (a.m <= 64) return launch_only<64, false>(a, stream);
+  if (a.m <= 96) return launch_cheapest<96, 128, false>(a, false, stream);
+  return launch_cheapest<128, 256, false>(a, a.m > 128, stream);
 }
 
 }  // namespace fi
