@@ -23,7 +23,7 @@
 // the pipeline's start and the cluster's end), of 248320 x 5120 184 us (6.9 TB/s), the gated form
 // at 16 rows of 2 x 17408 x 5120 30 us (6.0 TB/s). Up to 64 rows, and up to 96 where there are
 // tiles enough, two CTAs share an SM, so that one's loads cover the other's start and end; above, a
-// CTA has the SM's tensor memory to itself. 128 rows of 4096 x 14336 take 17.7 us, 256 rows 28.6.
+// CTA has the SM's tensor memory to itself. 128 rows of 4096 x 14336 take 17.9 us, 256 rows 28.8.
 //
 // Every wait is bounded. On a timeout the roles stop, the producer and the MMA issuer wait,
 // bounded, for what they have in flight, and every thread still meets the barriers.
