@@ -387,14 +387,30 @@ print("captured")
 def test_gated_waves_one_after_another(m, n, k):
     """Many CTAs, two on an SM, and calls that follow one another without a pause: an epilogue that falls
     behind its tensor core still sees every block."""
-    a = fi.quantize_fp8(torch.randn((m, k), generator=torch.Generator().manual_seed(m)).cuda())
-    w = fi.pack_weights_fp8(torch.randn((n, k), generator=torch.Generator().manual_seed(n)).cuda())
+    a = fi.quantize_fp8(_fp8.normal(m, k, 1).cuda())
+    w = fi.pack_weights_fp8(_fp8.normal(n, k, 2, 0.02).cuda())
     ref = fi.mm_fp8_gated(*a, *w, *w, out_dtype=torch.float32)
-    g = fi.mm_fp8(*a, *w, out_dtype=torch.float32).double()
-    # the two calls add the same blocks in fp32, in another order of K splits
-    tol = 2.0 ** -16 * (g.abs().amax() ** 2 + 1)
-    assert ((ref.double() - g * torch.sigmoid(g) * g).abs() <= tol).all()
+    g, gm = _fp8.product(a, w)
+    _fp8.check(ref, *(t.cpu() for t in _fp8.gated(g, gm, g, gm, k)))
     got = [fi.mm_fp8_gated(*a, *w, *w, out_dtype=torch.float32) for _ in range(40)]
     torch.cuda.synchronize()
     assert fi.get_device_error() == 0
     assert all(torch.equal(x, ref) for x in got)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k,gate", [(1000, 2506, 256, False), (1000, 2501, 256, False), (1030, 2500, 144, True),
+                                        (700, 3001, 128, True)])
+def test_outputs_of_any_pitch_and_start(dtype, m, n, k, gate):
+    """Many rows whose outputs start off a 16-byte boundary, and off a word; what is beside them stays."""
+    a, w, u = _whole(m, k, 1, 1), _whole(n, k, 128, 2), _whole(n, k, 128, 3)
+    w = (w[0], w[1] * 2.0 ** -8) if gate else w
+    (gr, gm), (ur, um) = _fp8.product(a, w), _fp8.product(a, u)
+    ref, tol = _fp8.gated(gr, 0 * gm, ur, 0 * um, k) if gate else (gr, 0 * gm)
+    a, w, u = _fp8.cuda(a), _fp8.cuda(w), _fp8.cuda(u)
+    for off in (0, 1, 2, 3, 4):
+        buf = torch.full((m * n + 16,), 7.0, device="cuda", dtype=dtype)
+        out = buf[off:off + m * n].view(m, n)
+        fi.mm_fp8_gated(*a, *w, *u, out=out) if gate else fi.mm_fp8(*a, *w, out=out)
+        _fp8.check(out, ref, tol)
+        assert bool((buf[:off] == 7).all()) and bool((buf[off + m * n:] == 7).all())
