@@ -27,7 +27,7 @@
 // shared memory (held in registers instead, one group ahead, and candidates inserted one by one it
 // was 111, 131, 186 and 262). 1024 x 152064 fp32 with 5 takes 122 us, 4096 x 32000 bf16 with 5 89
 // (inserted one by one: 117). One fp32 row of 152064 with 20 takes 13 us, most of it the latency of
-// the steps at its end (7.5 without the list).
+// the steps at its end (6.1 without the list).
 //
 // Masked entries: -inf, and what is below -2^26, is replaced by that value (kFloor), whose exponential
 // is 0 next to any maximum from -2^24 on; (z - M) exp(z - M) stays 0 instead of NaN. M log2 e is
@@ -51,7 +51,7 @@ constexpr int kMaxCtas = 8;  // of a row: a portable cluster
 constexpr int kSlots = 3;     // groups of vectors per warp that are on their way, or being used
 constexpr int kU = 4;         // vectors of a lane in a group
 constexpr int kFewTops = 8;   // up to here a limit comes from 32 maxima
-constexpr int kShort = 128, kMany = 256, kFew = 1024;  // threads of a CTA: many short rows, many rows, few rows
+constexpr int kShort = 128, kMany = 256, kFew = 1024;  // threads of a CTA: many rows, rows, few long rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -0x1p26f;  // stands for -inf and all below it (0xCC80 in bf16)
 constexpr float kFarMax = 0x1p24f;  // a greater magnitude of the row's maximum takes a second pass
@@ -744,19 +744,28 @@ int launch(const LogprobArgs& a, int ctas, cudaStream_t stream) {
 
 template <int DT>
 int launch_rows(const LogprobArgs& a, cudaStream_t stream) {
-  // CTAs per row: as many as leave each a group of vectors per warp, while the rows alone do not
-  // give every SM its CTAs
+  // CTAs per row: as many as leave each a group of vectors for most of its warps, while the rows alone
+  // do not give every SM its CTAs.
   const int64_t groups = a.vocab / Elem<DT>::kN / 128, sms = device_sm_count();
-  const bool few = a.rows * 16 <= sms && groups >= 8 * (kFew / 32) / 2;
+  // Few rows: large CTAs where the lists' limits are worth more threads. Measured (us, 256 threads /
+  // 1024): 33 bf16 rows of 100000 with 5 alternatives 11.2 / 10.0, with 20 15.2 / 11.4, fp32 17.0 / 13.5;
+  // 100 rows with 20 19.3 / 17.0, with 5 14.4 / 14.3; one row of 152064 with 5 8.9 / 10.9,
+  // fp32 9.7 / 10.9, of 260000 12.1 / 11.4.
+  const bool few = a.topk > kFewTops ? a.rows <= sms && groups >= 64
+                                     : (a.rows * 16 <= sms ? groups >= 400 : a.topk > 0 && a.rows * 4 <= sms && groups >= 64);
   // Many rows: with small CTAs fewer warps wait at a row's start and end, with large ones the last
   // wave is shorter and the lists' limits come from more threads. Measured with 128 / 256 threads
-  // (us): 4096 rows of 32000 with 5 alternatives 89 / 107, of 5001 38 / 65, 2047 of 152064 without
-  // a list 99 / 111, with 32 217 / 212; 1024 fp32 rows of 152064 with 5 135 / 122.
-  if ((groups < 32 || a.topk == 0) && a.rows >= 8 * sms) return launch<DT, kShort>(a, 1, stream);
-  const int64_t warps = (few ? kFew : kMany) / 32, slots = few ? sms : 768 / kMany * sms;
+  // (us): 4096 rows of 32000 with 5 alternatives 89 / 107, of 5001 38 / 65, 1000 of 5000 with 20 17.4 /
+  // 25.4, 2047 of 152064 without a list 99 / 111, with 32 217 / 212, 3600 of
+  // 100000 with 20 234 / 263; 1024 fp32 rows of 152064 with 5 135 / 122, 3600 of 25000 85 / 101.
+  const int64_t small = 768 / kShort * sms, large = 768 / kMany * sms;  // CTAs that the device holds
+  const bool fewer_waves = (a.rows + small - 1) / small * small * 100 <= (a.rows + large - 1) / large * large * 118;
+  if (a.rows > large && (groups < 32 || (a.topk == 0 ? a.rows >= 8 * sms : fewer_waves)))
+    return launch<DT, kShort>(a, 1, stream);
+  const int64_t warps = (few ? kFew : kMany) / 32, slots = few ? sms : large;
   int ctas = 1;
   static_assert(kMany / 32 >= kMaxCtas && kFew / 32 >= kMaxCtas, "a warp takes the list of each CTA of a cluster");
-  while (ctas < kMaxCtas && a.rows * ctas * 2 <= slots && groups >= ctas * 2 * warps / 2) ctas *= 2;
+  while (ctas < kMaxCtas && a.rows * ctas * 2 <= slots && groups >= ctas * warps + 4) ctas *= 2;
   return few ? launch<DT, kFew>(a, ctas, stream) : launch<DT, kMany>(a, ctas, stream);
 }
 
