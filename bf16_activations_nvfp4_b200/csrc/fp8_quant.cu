@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(512, DT == FI_DTYPE_F32 ? 2 : 4) fp8_quant_squ
                                                                uint32_t kblocks, int64_t k, uint8_t* __restrict__ q,
                                                                float* __restrict__ scale) {
   constexpr int kN = Vec<DT>::kN, kLanes = kFp8Block / kN, kEs = 16 / kN, kU = 32 / kN;
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t rb = blockIdx.x / kblocks, cb = blockIdx.x - rb * kblocks;
   const int64_t e = cb * kFp8Block + (threadIdx.x % kLanes) * kN;
   const int64_t r0 = rb * kFp8Block + threadIdx.x / kLanes;
@@ -247,11 +249,20 @@ template <int DT>
 int launch_quantize(const uint8_t* x, int64_t rows, int64_t k, bool square, uint8_t* q, float* scale,
                     cudaStream_t stream) {
   const int64_t kb = fp8_blocks(k);
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (square) {
     const int64_t grid = fp8_blocks(rows) * kb;
     if (grid > 0x7fffffffLL) return set_error(FI_ERR_UNSUPPORTED_SHAPE, "weight tensor too large");
-    fp8_quant_square_kernel<DT><<<(unsigned)grid, 512, 0, stream>>>(x, rows, (uint32_t)kb, k, q, scale);
-    if (cudaGetLastError() != cudaSuccess) return set_cuda_error("fp8_quant_square_kernel launch");
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(512);
+    if (cudaLaunchKernelEx(&cfg, fp8_quant_square_kernel<DT>, x, rows, (uint32_t)kb, k, q, scale) != cudaSuccess)
+      return set_cuda_error("fp8_quant_square_kernel launch");
     return FI_OK;
   }
   const int64_t groups = rows * kb, per_cta = 256 / (kFp8Block / Vec<DT>::kN);
@@ -259,15 +270,8 @@ int launch_quantize(const uint8_t* x, int64_t rows, int64_t k, bool square, uint
   const bool deep = groups >= (int64_t)device_sm_count() * 2 * per_cta * 4;
   const int64_t grid = (groups + per_cta * (deep ? 4 : 1) - 1) / (per_cta * (deep ? 4 : 1));
   if (grid > 0x7fffffffLL) return set_error(FI_ERR_UNSUPPORTED_SHAPE, "activation tensor too large");
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const bool whole = k % kFp8Block == 0;
   auto kern = deep ? (whole ? fp8_quant_rows_kernel<DT, 4, true> : fp8_quant_rows_kernel<DT, 4, false>)
                    : (whole ? fp8_quant_rows_kernel<DT, 1, true> : fp8_quant_rows_kernel<DT, 1, false>);
