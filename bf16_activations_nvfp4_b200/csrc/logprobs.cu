@@ -694,14 +694,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFew ? 1 : 768 / kThread
   }
   if (warp != 0) return;
   const bool empty = a.s == 0.0f;  // nothing but -inf
-  const float log2_s = empty ? 0.0f : __log2f(a.s), mean = empty ? 0.0f : a.t / a.s;
-  // ln(sum exp(z - m)): the point is off m log2 e by its rounding (of a far row the sums are relative
-  // to the maximum itself, t in natural units)
-  const float ln_sum = (far ? log2_s : log2_s - fmaf(a.m, kLog2e, -point(a.m))) * kLn2;
+  // The point is off m log2 e by its rounding, `off`, and every exponential by the power of two of that
+  // (of a far row the sums are relative to the maximum itself, t in natural units). s is divided by the
+  // maximum's own exponential, as the loop found it: s holds it, so the quotient is 1 at least and just
+  // that where the other entries add nothing, and its logarithm 0. With t's true value at most 0, no log
+  // probability comes out above 0 and no entropy below, and a row with one entry left has 0 for both.
+  const float off = far ? 0.0f : fmaf(a.m, kLog2e, -point(a.m));
+  const float ln_sum = empty ? 0.0f : logf(a.s / exp2_fast(off));
+  const float t = __fsub_rn(a.t, __fmul_rn(off, a.s));
+  const float mean = empty ? 0.0f : (t > 0.0f ? 0.0f : t) / a.s * (far ? 1.0f : kLn2);
   auto logprob_of = [&](float x) { return empty ? x : (x - a.m) - ln_sum; };
   if (lane == 0) {
     p.logprob[row] = has_token ? logprob_of(zt) : __uint_as_float(0x7FC00000u);
-    p.entropy[row] = far ? log2_s * kLn2 - mean : (log2_s - mean) * kLn2;
+    p.entropy[row] = ln_sum - mean;
     p.rank[row] = has_token ? (int64_t)earlier : -1;
   }
   if (lane < K) {

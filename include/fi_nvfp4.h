@@ -335,6 +335,7 @@ FI_API int fi_mm_fp8_gated(const uint8_t* Aq, const float* Ascale, const uint8_t
  *   logprob, entropy  device fp32 [rows] (outputs).
  *   rank          device int64 [rows] (output).
  *   top_logprobs, top_ids  device fp32 / int64 [rows, min(topk, vocab)] (outputs; unused if topk == 0).
+ * No logprob is above 0 and no entropy below; a row with one entry left has 0 for both.
  * An entry of -inf is masked: it has probability 0 and adds nothing. A row of nothing else has
  * logprob -inf and entropy 0. A row that holds NaN or +inf has NaN logprob and entropy; NaN comes
  * first in the order. A token outside [0, vocab) has logprob NaN and rank -1.
