@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     }
     if (GATED) {
       const float4 u = v[G::kTiles - 1];
-      v[0] = make_float4(silu(v[0].x) * u.x, silu(v[0].y) * u.y, silu(v[0].z) * u.z, silu(v[0].w) * u.w);
+      silu_times(v[0].x, v[0].y, u.x, u.y);
+      silu_times(v[0].z, v[0].w, u.z, u.w);
     }
     if (j < p.n) store_out4(p.out, p.out_dtype, (m0 + e / (kTileRows / 4)) * p.n + j, v[0], wide, p.n - j);
   }

@@ -21,7 +21,8 @@
 // Bound by the chain of a block's steps (MMAs, commit, TMEM loads, additions, release: two TMEM
 // buffers are in flight) and, under sustained load, by power: 720 to 750 cycles per block of a pair
 // where the MMAs and loads alone take 638 and the nominal rate is 512. 8192 x 4096 x 14336 takes
-// 404 us (2.4 PFLOP/s), 470 at the power limit; 4096 rows of the gated 2 x 17408 x 5120 685 us.
+// 404 us (2.4 PFLOP/s), 470 at the power limit; 4096 rows of the gated 2 x 17408 x 5120 617 us in 20
+// calls, 721 at the power limit.
 // N = 128 instructions with four buffers took 646 us on the former where this form took 504, 16
 // epilogue warps 559 against 450.
 //
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t row0 = ((int64_t)tm * 2 + rank) * kRows + quarter * 32;
         if (GATED) {  // the first 64 columns are gates, the others their up columns
 #pragma unroll
-          for (int c = 0; c < 64; ++c) acc[c] = silu(acc[c]) * acc[64 + c];
+          for (int c = 0; c < 64; c += 2) silu_times(acc[c], acc[c + 1], acc[64 + c], acc[65 + c]);
           store_rows<0, OUT>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 128 + half * 64);
         } else {
           store_rows<0, OUT>(p, w.wide_stores != 0, acc, stage, lane, row0, (int64_t)tn * 256 + half * 64);

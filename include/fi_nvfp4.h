@@ -313,7 +313,8 @@ FI_API int fi_mm_fp8(const uint8_t* Aq, const float* Ascale, const uint8_t* Wq, 
 /*
  * The first half of a gated feed-forward block in one kernel:
  *     out[i][j] = round(g / (1 + exp(-g)) * u),   g = (A G^T)[i][j], u = (A U^T)[i][j]
- * with g and u the fp32 sums of fi_mm_fp8, never rounded in between. G and U are two weights
+ * with g and u the fp32 sums of fi_mm_fp8, never rounded in between. g / (1 + exp(-g)) is found in
+ * fp32, within 7 units (2^-23) for every g (below 2^-126: a few of 2^-149). G and U are two weights
  * [n, k] with their scales (of a fused [2n, k] weight with n a multiple of 128, its two halves).
  * Other arguments and preconditions are those of fi_mm_fp8.
  */
