@@ -26,7 +26,9 @@
 // CTA has the SM's tensor memory to itself. 128 rows of 4096 x 14336 take 17.9 us, 256 rows 28.8.
 //
 // Every wait is bounded. On a timeout the roles stop, the producer and the MMA issuer wait,
-// bounded, for what they have in flight, and every thread still meets the barriers.
+// bounded, for what they have in flight, and every thread still meets the barriers. Every role waits for the
+// end of the preceding kernel before its first bounded wait, so that a limit never counts another
+// kernel's time.
 #include <cstdint>
 #include <algorithm>
 #include <atomic>
@@ -167,6 +169,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
     if (lane == 0) {
       constexpr uint32_t idesc = f8_idesc(kTileRows, N);
       bool ok = true;
+      pdl_wait();  // the limit of a wait counts from the preceding kernel's end
       for (int i = 0; i < KB; ++i) {
         const int st = i % G::kStages, b = i % G::kBufs;
         ok = mbar_wait_spin(&full[st], (i / G::kStages) & 1, &abort_flag, p.timeout_ns, p.err, 1u) &&
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       if (lane == 0) mbar_arrive(&scale_full[g]);
     }
   } else {
+    pdl_wait();  // before the first wait with a limit, and before any output is written
     const int epi = warp - kWarpEpi0, quarter = warp & 3, group = epi >> 2;
     const int tile = GATED ? group : 0;
     const int c0 = GATED ? 0 : group * G::kCols;  // first activation row (column) of this thread

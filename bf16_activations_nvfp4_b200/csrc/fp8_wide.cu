@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (lane == 0 && rank == 0) {
         constexpr uint32_t idesc = f8_idesc(256, 256);
+        pdl_wait();  // the limit of a wait counts from the preceding kernel's end
         const int64_t total = my_tiles * KB;
         int st = 0;
         uint32_t phase = 0;
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    pdl_wait();  // before the first wait with a limit, and before any output is written
     const int epi = warp - 4, quarter = warp & 3, half = epi >> 2;
     uint8_t* const stage = staging + epi * (kOutBytes / 8);
     const uint32_t empty0 = map_to(smem_addr(tmem_empty), 0);
