@@ -123,10 +123,6 @@ __device__ __forceinline__ void fma_scaled(float& x, float& y, uint32_t a, uint3
       : "r"(a), "r"(b), "l"(s));
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Four fp32 at `addr` (a shared-memory address of this CTA) in the cluster's CTA `rank`.
 __device__ __forceinline__ float4 ld_dsmem_v4(uint32_t addr, uint32_t rank) {
   uint32_t remote;

@@ -265,17 +265,6 @@ __device__ __forceinline__ T merge32(T list, T asc, int lane) {
   return v;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
-  uint32_t remote, v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote));
-  return v;
-}
-
 __device__ __forceinline__ uint64_t ld_dsmem_u64(const void* p, uint32_t rank) {
   uint32_t remote;
   uint64_t v;

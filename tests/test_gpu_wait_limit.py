@@ -68,3 +68,25 @@ def test_products_in_a_row_behind_a_long_kernel(long_call):
     a = fi.quantize_fp8(_fp8.normal(40, 1024, 1).cuda())
     w = fi.pack_weights_fp8(_fp8.normal(1024, 1024, 2, 0.02).cuda())
     _behind(long_call, lambda: fi.mm_fp8(*fi.quantize_fp8(fi.mm_fp8(*a, *w)), *w))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 4096), (30, 3000, 1024), (64, 3000, 1024), (80, 20480, 1024),
+                                   (128, 2048, 2048), (200, 512, 1024), (256, 4096, 14336), (1024, 8192, 1024)])
+@pytest.mark.parametrize("gate", [False, True])
+def test_nothing_is_stored_when_a_wait_ran_out(m, n, k, gate):
+    mark = 2.0 ** 100  # far above what the product can give
+    a = fi.quantize_fp8(_fp8.normal(m, k, 1).cuda())
+    w = fi.pack_weights_fp8(_fp8.normal(n, k, 2, 0.02).cuda())
+    out = torch.full((m, n), mark, dtype=torch.bfloat16, device="cuda")
+    call = lambda: fi.mm_fp8_gated(*a, *w, *w, out=out) if gate else fi.mm_fp8(*a, *w, out=out)
+    with short_limit():
+        fi.debug_set(fi.DEBUG_STALL_PRODUCER, 1)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            fi.debug_set(fi.DEBUG_STALL_PRODUCER, 0)
+    assert fi.get_device_error() != 0
+    assert bool((out == mark).all())
+    call()
+    assert fi.get_device_error() == 0 and not bool((out == mark).any())
