@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(GemvArgs p)
       int64_t issued = 0;
       for (int64_t q = 0; q < Q; ++q) {
         const int slot = (int)(q % NST);
+        if (q == NST) pdl_wait();  // the limit of a wait counts from the preceding kernel's end
         if (q >= NST && !mbar_wait_bounded(&empty[slot], (uint32_t)((q / NST - 1) & 1), &abort_flag,
                                            p.timeout_ns, 2u))
           break;

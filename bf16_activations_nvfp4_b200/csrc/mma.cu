@@ -383,6 +383,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       }
       for (int s = 0; s + kRawStages < KS && !abort_flag; ++s) {
         const int rs = s % kRawStages;
+        // The limit of a wait counts from the preceding kernel's end, here and in the other roles: each
+        // waits for that before its first wait on what the MMAs do, which need the activations.
+        if (s == NST) pdl_wait();
         if (!mbar_wait_bounded(&raw_empty[rs], (uint32_t)((s / kRawStages) & 1), &abort_flag, p.timeout_ns, p.err,
                                2u))
           break;
@@ -476,6 +479,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           // them saw both.
           const bool fast = mbar_try_wait(&raw_full[j], par) && (s0 == 0 || mbar_try_wait(&op_empty[j], par ^ 1u));
           if (!__all_sync(0xffffffffu, fast)) {
+            if (s0 != 0) pdl_wait();
             const bool ok = mbar_wait_bounded(&raw_full[j], par, &abort_flag, p.timeout_ns, p.err, 1u) &&
                             (s0 == 0 || mbar_wait_bounded(&op_empty[j], par ^ 1u, &abort_flag, p.timeout_ns, p.err, 1u));
             if (!__all_sync(0xffffffffu, ok)) {
@@ -514,7 +518,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         // seen lane by lane, and the warp must stay converged for __syncwarp below)
         const bool ok =
             mbar_wait_bounded(&raw_full[rsn], (uint32_t)((s / kRawStages) & 1), &abort_flag, p.timeout_ns, p.err, 1u) &&
-            (s < NST || mbar_wait_bounded(&op_empty[os], eph, &abort_flag, p.timeout_ns, p.err, 1u));
+            (s < NST || mbar_try_wait(&op_empty[os], eph) ||
+             (pdl_wait(), mbar_wait_bounded(&op_empty[os], eph, &abort_flag, p.timeout_ns, p.err, 1u)));
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint4 c0 = lds_v4m(raw_addr(rsn) + (uint32_t)r * 32u + (uint32_t)hb * 16u);
         uint32_t hv[16];  // the 32 k of this thread as f16 pairs, in k order
@@ -557,6 +562,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       const uint32_t b_res_step = (uint32_t)N * 8u;
       int os = 0;
       uint32_t par = 0;  // phase of act_full[os] and op_full[os] for step s
+      pdl_wait();
       bool go = !resident || mbar_wait_bounded(&act_full[0], 0u, &abort_flag, p.timeout_ns, p.err, 4u);
       for (int s = 0; s < KS && go; ++s) {
         if (!resident && !mbar_wait_bounded(&act_full[os], par, &abort_flag, p.timeout_ns, p.err, 4u)) break;

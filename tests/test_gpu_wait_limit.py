@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import bf16_activations_nvfp4_b200 as fi
-from tests import _fp8
+from tests import _fp8, _gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,16 @@ def test_nothing_is_stored_when_a_wait_ran_out(m, n, k, gate):
     assert bool((out == mark).all())
     call()
     assert fi.get_device_error() == 0 and not bool((out == mark).any())
+
+
+# the GEMV's ring with and without K splits; the tensor-core path with either activation mode, and with
+# the decoded weights in tensor memory (up to 128 rows) or in shared memory
+@pytest.mark.parametrize("m,n,k,tactic", [
+    (1, 4096, 14336, fi.make_tactic(fi.KIND_GEMV, 1, 0, 0x22)), (2, 1024, 14336, fi.make_tactic(fi.KIND_GEMV, 4, 0, 0x22)),
+    (1, 4096, 14336, fi.TACTIC_DEFAULT), (8, 4096, 14336, fi.make_tactic(fi.KIND_MMA, 1, 0, 1)),
+    (8, 4096, 14336, fi.make_tactic(fi.KIND_MMA, 8, 0, 2)), (200, 4096, 4096, fi.make_tactic(fi.KIND_MMA, 1, 0, 1)),
+    (200, 4096, 4096, fi.TACTIC_DEFAULT)])
+def test_4_bit_products_behind_a_long_kernel(long_call, m, n, k, tactic):
+    weights = _gpu.device_weights(n, k, 3)
+    x = _fp8.normal(m, k, 1).to(torch.bfloat16).cuda()
+    _behind(long_call, lambda: fi.mm_bf16_fp4(x, *weights, tactic=tactic))
