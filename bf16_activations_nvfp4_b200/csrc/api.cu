@@ -697,8 +697,7 @@ static int mm_run(const uint16_t* A, const uint8_t* Wq, const uint8_t* Wscale, c
     // overlapped pipeline: weights that fit the L2 with room to spare (two consecutive calls'
     // worth) are prefetched into it whole at kernel start, while the preceding call computes
     a.prefetch_l2 = g.pipeline == kPipeOverlap && n * (k / 2 + k / 16) <= ((int64_t)40 << 20) ? 1 : 0;
-    a.debug_stall = g_debug_stall_launches > 0 ? 1 : 0;
-    if (g_debug_stall_launches > 0) --g_debug_stall_launches;
+    a.debug_stall = take_debug_stall();
     a.stage_bytes = g.stage_bytes;
     a.off_as = g.off_as;
     a.off_bar = g.off_bar;
@@ -737,8 +736,7 @@ static int mm_run(const uint16_t* A, const uint8_t* Wq, const uint8_t* Wscale, c
       a.op_stages = mma_op_stages(a.m_pad);
       a.stage_bytes = (uint32_t)mma_stage_bytes(a.m_pad);
     }
-    a.debug_stall = g_debug_stall_launches > 0 ? 1 : 0;
-    if (g_debug_stall_launches > 0) --g_debug_stall_launches;
+    a.debug_stall = take_debug_stall();
     a.err = device_error_word();
     if (!a.err) return set_cuda_error("cudaGetSymbolAddress(device error word)");
     a.timeout_ns = g_wait_timeout_ns;
