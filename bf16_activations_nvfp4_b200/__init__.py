@@ -385,7 +385,14 @@ def _load_binding():
             if not os.path.exists(path):
                 raise RuntimeError(f"{path} is missing: build it with `python -m bf16_activations_nvfp4_b200.build` "
                                    "(there is no fallback implementation)")
-            from . import _binding
+            try:
+                from . import _binding
+                built = _binding.torch_version
+            except (ImportError, AttributeError) as e:
+                built = str(e)
+            if built != torch.__version__:
+                raise RuntimeError(f"{path} was built for another torch than {torch.__version__} ({built}): build it "
+                                   "with `python -m bf16_activations_nvfp4_b200.build`")
             _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.fi_fp8_quantize, lib.fi_fp8_pack_weights, lib.fi_mm_fp8, lib.fi_mm_fp8_gated,
                 lib.fi_token_logprobs)))

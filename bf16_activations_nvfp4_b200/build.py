@@ -25,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfi_nvfp4.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_RECORD = os.path.join(BUILD, "binding.command")  # what BINDING was built with
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -59,9 +60,19 @@ def _binding_command(nvcc: str, target: str) -> list[str]:
     paths = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
     # torch's libraries are in the process before the module is: no run path
     return [shutil.which("g++") or "g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-isystem" + p for p in paths],
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DFI_TORCH_VERSION="{torch.__version__}"', *["-isystem" + p for p in paths],
             os.path.join(CSRC, "binding.cpp"), "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
             "-ltorch_python", "-o", target]
+
+
+def _binding_stale(record: str) -> bool:
+    """The module uses torch's C++ interface: another torch, Python or compiler call needs another one."""
+    sources = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "fi_nvfp4.h"), __file__]
+    if _stale(BINDING, sources) or not os.path.exists(BINDING_RECORD):
+        return True
+    with open(BINDING_RECORD) as f:
+        return f.read() != record
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -78,8 +89,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             jobs.append([nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj])
     link = force or bool(jobs)
     binding_tmp = BINDING + f".tmp{os.getpid()}"
-    binding_sources = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "fi_nvfp4.h"), __file__]
-    binding = force or _stale(BINDING, binding_sources)
+    record = " ".join(_binding_command(nvcc, BINDING))
+    binding = force or _binding_stale(record)
     if binding:
         jobs.append(_binding_command(nvcc, binding_tmp))
 
@@ -95,6 +106,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         list(ex.map(run, jobs))
     if binding:
         os.replace(binding_tmp, BINDING)
+        with open(BINDING_RECORD, "w") as f:
+            f.write(record)
     if link or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
