@@ -33,7 +33,8 @@ import torch
 __all__ = [
     "FiError", "KIND_GEMV", "KIND_MMA", "TACTIC_DEFAULT", "make_tactic", "tactic_fields",
     "pack_weights", "mm_bf16_fp4", "splitk_reduce", "quantize_fp8", "pack_weights_fp8", "mm_fp8",
-    "mm_fp8_gated", "token_logprobs", "lm_head_logprobs", "TokenLogprobs", "FP8_BLOCK", "MAX_TOPK", "resolve_tactic", "default_tactic",
+    "mm_fp8_gated", "token_logprobs", "lm_head_logprobs", "TokenLogprobs", "FP8_BLOCK", "MAX_TOPK",
+    "MAX_FP8_SPLITS", "resolve_tactic", "default_tactic",
     "list_tactics", "workspace_bytes", "set_workspace", "last_error", "version", "library",
     "library_path", "get_device_error", "debug_set", "DEBUG_STALL_PRODUCER", "DEBUG_WAIT_TIMEOUT_NS",
 ]
@@ -50,6 +51,7 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _DTYPES_ANY = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 FP8_BLOCK = 128  # k (and weight rows) per scale
 MAX_TOPK = 32    # FI_LOGPROBS_MAX_TOPK
+MAX_FP8_SPLITS = 8  # FI_FP8_MAX_SPLITS
 
 _STATUS = {0: "FI_OK", -1: "FI_ERR_INVALID_ARG", -2: "FI_ERR_UNSUPPORTED_SHAPE",
            -3: "FI_ERR_UNSUPPORTED_ARCH", -4: "FI_ERR_WORKSPACE", -5: "FI_ERR_CUDA"}
@@ -110,6 +112,8 @@ def library() -> ctypes.CDLL:
         lib.fi_fp8_pack_weights.argtypes = [vp, ci, i64, i64, vp, vp, vp]
         lib.fi_mm_fp8.argtypes = [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp]
         lib.fi_mm_fp8_gated.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, vp]
+        lib.fi_mm_fp8_ex.argtypes = [vp, vp, vp, vp, vp, ci, i64, i64, i64, ci, vp]
+        lib.fi_mm_fp8_gated_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, ci, vp]
         lib.fi_token_logprobs.argtypes = [vp, ci, i64, i64, i64, vp, ci, vp, vp, vp, vp, vp, vp]
         lib.fi_resolve_tactic.argtypes = [i64, i64, i64, i64, ctypes.c_int, ctypes.POINTER(TacticInfo)]
         lib.fi_default_tactic.argtypes = [i64, i64, i64, ctypes.c_int]
@@ -125,7 +129,8 @@ def library() -> ctypes.CDLL:
         lib.fi_debug_set.argtypes = [ctypes.c_int, i64]
         for name in ("fi_nvfp4_pack_weights", "fi_mm_bf16_fp4", "fi_mm_bf16_fp4_ex", "fi_mm_bf16_fp4_noalloc",
                      "fi_splitk_reduce", "fi_mm_bf16_fp4_out", "fi_splitk_reduce_out", "fi_fp8_quantize",
-                     "fi_fp8_pack_weights", "fi_mm_fp8", "fi_mm_fp8_gated", "fi_token_logprobs",
+                     "fi_fp8_pack_weights", "fi_mm_fp8", "fi_mm_fp8_gated", "fi_mm_fp8_ex",
+                     "fi_mm_fp8_gated_ex", "fi_token_logprobs",
                      "fi_resolve_tactic", "fi_list_tactics", "fi_set_workspace", "fi_version",
                      "fi_get_device_error", "fi_debug_set"):
             getattr(lib, name).restype = ctypes.c_int
@@ -394,7 +399,7 @@ def _load_binding():
                 raise RuntimeError(f"{path} was built for another torch than {torch.__version__} ({built}): build it "
                                    "with `python -m bf16_activations_nvfp4_b200.build`")
             _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.fi_fp8_quantize, lib.fi_fp8_pack_weights, lib.fi_mm_fp8, lib.fi_mm_fp8_gated,
+                lib.fi_fp8_quantize, lib.fi_fp8_pack_weights, lib.fi_mm_fp8_ex, lib.fi_mm_fp8_gated_ex,
                 lib.fi_token_logprobs)))
             _native = _binding
     return _native
@@ -452,7 +457,7 @@ def _fp8_operand(q: torch.Tensor, s: torch.Tensor, k: int | None, rows: int, qn:
 
 
 def _refuse_product(Aq: torch.Tensor, Ascale: torch.Tensor, weights: dict, out: torch.Tensor | None,
-                    out_dtype: torch.dtype | None):
+                    out_dtype: torch.dtype | None, splits: int):
     """Raises what is wrong with a product's arguments; `weights` are its codes and scales by name."""
     m, k = _fp8_operand(Aq, Ascale, None, 1, "Aq", "Ascale")
     n = None
@@ -463,6 +468,8 @@ def _refuse_product(Aq: torch.Tensor, Ascale: torch.Tensor, weights: dict, out: 
             raise ValueError(f"Gq has {n} rows and {name} {r}")
         n = r
     _same_device(Aq, Ascale=Ascale, **weights)
+    if not isinstance(splits, int):
+        raise TypeError(f"splits must be an int, got {type(splits).__name__}")
     dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
     if dtype not in _DTYPES_ANY or (out_dtype is not None and out_dtype != dtype):
         raise ValueError(f"the output is bf16, f16 or fp32 (out_dtype {out_dtype}, out "
@@ -473,25 +480,27 @@ def _refuse_product(Aq: torch.Tensor, Ascale: torch.Tensor, weights: dict, out: 
 
 
 def mm_fp8(Aq: torch.Tensor, Ascale: torch.Tensor, Wq: torch.Tensor, Wscale: torch.Tensor,
-           out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+           out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, splits: int = 0) -> torch.Tensor:
     """out[m, n] = (Aq scaled by Ascale) . (Wq scaled by Wscale)^T for codes and scales of
     quantize_fp8 and pack_weights_fp8; fp32 sums, bf16 out unless out_dtype (or the dtype of
-    `out`) is torch.float16 or torch.float32. Any m; k a multiple of 16."""
-    r = (_native or _load_binding()).mm(Aq, Ascale, Wq, Wscale, out, out_dtype)
+    `out`) is torch.float16 or torch.float32. Any m; k a multiple of 16. `splits` (1 to
+    MAX_FP8_SPLITS) fixes the K splits: a row's bits then do not depend on how many rows there are; 0
+    chooses them by the sizes."""
+    r = (_native or _load_binding()).mm(Aq, Ascale, Wq, Wscale, out, out_dtype, splits)
     if r is None:
-        _refuse_product(Aq, Ascale, {"Wq": Wq, "Wscale": Wscale}, out, out_dtype)
+        _refuse_product(Aq, Ascale, {"Wq": Wq, "Wscale": Wscale}, out, out_dtype, splits)
     return _done(r, "fi_mm_fp8")
 
 
 def mm_fp8_gated(Aq: torch.Tensor, Ascale: torch.Tensor, Gq: torch.Tensor, Gscale: torch.Tensor,
                  Uq: torch.Tensor, Uscale: torch.Tensor, out: torch.Tensor | None = None,
-                 out_dtype: torch.dtype | None = None) -> torch.Tensor:
+                 out_dtype: torch.dtype | None = None, splits: int = 0) -> torch.Tensor:
     """silu(A G^T) * (A U^T) [m, n] in one kernel, both products as mm_fp8 computes them and not
     rounded before the activation. G and U are [n, k]; of a fused [2n, k] weight with n a multiple
-    of 128, pass the two halves of its codes and scales."""
-    r = (_native or _load_binding()).gated(Aq, Ascale, Gq, Gscale, Uq, Uscale, out, out_dtype)
+    of 128, pass the two halves of its codes and scales. `splits` as in mm_fp8."""
+    r = (_native or _load_binding()).gated(Aq, Ascale, Gq, Gscale, Uq, Uscale, out, out_dtype, splits)
     if r is None:
-        _refuse_product(Aq, Ascale, {"Gq": Gq, "Gscale": Gscale, "Uq": Uq, "Uscale": Uscale}, out, out_dtype)
+        _refuse_product(Aq, Ascale, {"Gq": Gq, "Gscale": Gscale, "Uq": Uq, "Uscale": Uscale}, out, out_dtype, splits)
     return _done(r, "fi_mm_fp8_gated")
 
 

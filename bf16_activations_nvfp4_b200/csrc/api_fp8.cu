@@ -36,11 +36,13 @@ static int quantize(const void* x, int dtype, int64_t rows, int64_t k, bool squa
 }
 
 static int product(const uint8_t* A, const float* As, const uint8_t* W0, const float* Ws0, const uint8_t* W1,
-                   const float* Ws1, bool gated, void* out, int out_dtype, int64_t m, int64_t n, int64_t k,
+                   const float* Ws1, bool gated, void* out, int out_dtype, int64_t m, int64_t n, int64_t k, int splits,
                    fi_stream_t stream) {
   clear_error();
   if (!known_dtype(out_dtype)) return set_error(FI_ERR_INVALID_ARG, "out_dtype %d is not an fi_dtype", out_dtype);
   if (m < 0 || n < 0 || k < 0) return set_error(FI_ERR_INVALID_ARG, "negative size");
+  if (splits < 0 || splits > kFp8MaxSplits)
+    return set_error(FI_ERR_INVALID_ARG, "splits=%d is not in [0, %d]", splits, kFp8MaxSplits);
   if (k % 16 != 0) return set_error(FI_ERR_UNSUPPORTED_SHAPE, "k=%lld is not a multiple of 16", (long long)k);
   if (!product_fits(m, n) || !product_fits(m, k) || !product_fits(n, k))
     return set_error(FI_ERR_UNSUPPORTED_SHAPE, "m=%lld n=%lld k=%lld is too large", (long long)m, (long long)n,
@@ -78,7 +80,7 @@ static int product(const uint8_t* A, const float* As, const uint8_t* W0, const f
   a.n = n;
   a.k = k;
   a.kblocks = (int)fp8_blocks(k);
-  return launch_fp8_mm(a, gated, reinterpret_cast<cudaStream_t>(stream));
+  return launch_fp8_mm(a, gated, splits, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace fi
@@ -98,13 +100,24 @@ int fi_fp8_pack_weights(const void* W, int dtype, int64_t n, int64_t k, uint8_t*
 
 int fi_mm_fp8(const uint8_t* Aq, const float* Ascale, const uint8_t* Wq, const float* Wscale, void* out, int out_dtype,
               int64_t m, int64_t n, int64_t k, fi_stream_t stream) {
-  return product(Aq, Ascale, Wq, Wscale, nullptr, nullptr, false, out, out_dtype, m, n, k, stream);
+  return product(Aq, Ascale, Wq, Wscale, nullptr, nullptr, false, out, out_dtype, m, n, k, 0, stream);
+}
+
+int fi_mm_fp8_ex(const uint8_t* Aq, const float* Ascale, const uint8_t* Wq, const float* Wscale, void* out,
+                 int out_dtype, int64_t m, int64_t n, int64_t k, int splits, fi_stream_t stream) {
+  return product(Aq, Ascale, Wq, Wscale, nullptr, nullptr, false, out, out_dtype, m, n, k, splits, stream);
 }
 
 int fi_mm_fp8_gated(const uint8_t* Aq, const float* Ascale, const uint8_t* Gq, const float* Gscale, const uint8_t* Uq,
                     const float* Uscale, void* out, int out_dtype, int64_t m, int64_t n, int64_t k,
                     fi_stream_t stream) {
-  return product(Aq, Ascale, Gq, Gscale, Uq, Uscale, true, out, out_dtype, m, n, k, stream);
+  return product(Aq, Ascale, Gq, Gscale, Uq, Uscale, true, out, out_dtype, m, n, k, 0, stream);
+}
+
+int fi_mm_fp8_gated_ex(const uint8_t* Aq, const float* Ascale, const uint8_t* Gq, const float* Gscale,
+                       const uint8_t* Uq, const float* Uscale, void* out, int out_dtype, int64_t m, int64_t n,
+                       int64_t k, int splits, fi_stream_t stream) {
+  return product(Aq, Ascale, Gq, Gscale, Uq, Uscale, true, out, out_dtype, m, n, k, splits, stream);
 }
 
 int fi_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const int64_t* tokens,

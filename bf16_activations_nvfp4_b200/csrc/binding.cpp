@@ -26,8 +26,8 @@ namespace {
 constexpr int64_t kBlock = 128;  // k (and weight rows) per scale
 
 decltype(&fi_fp8_quantize) quantize_fn, pack_fn;
-decltype(&fi_mm_fp8) mm_fn;
-decltype(&fi_mm_fp8_gated) gated_fn;
+decltype(&fi_mm_fp8_ex) mm_fn;
+decltype(&fi_mm_fp8_gated_ex) gated_fn;
 decltype(&fi_token_logprobs) logprobs_fn;
 
 int64_t blocks(int64_t x) { return (x + kBlock - 1) / kBlock; }
@@ -132,34 +132,45 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (Aq, Ascale, Wq, Wscale, out, out_dtype)
+// An int argument; what no C int holds becomes -1, for the library to refuse.
+bool number(PyObject* o, int* v) {
+  if (!PyLong_Check(o)) return false;
+  int overflow = 0;
+  const long x = PyLong_AsLongAndOverflow(o, &overflow);
+  *v = overflow || x < 0 || x > 0x7fffffffL ? -1 : (int)x;
+  return true;
+}
+
+// (Aq, Ascale, Wq, Wscale, out, out_dtype, splits)
 PyObject* mm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Operand x, w;
   at::Tensor out;
-  if (n != 6 || !x.get(a[0], a[1], 1) || !w.get(a[2], a[3], kBlock) || w.k != x.k ||
+  int splits;
+  if (n != 7 || !number(a[6], &splits) || !x.get(a[0], a[1], 1) || !w.get(a[2], a[3], kBlock) || w.k != x.k ||
       w.q->get_device() != x.q->get_device() || !output(a[4], a[5], x.r, w.r, x.q->get_device(), &out))
     Py_RETURN_NONE;
   const int rc = call(x.q->get_device(), [&](fi_stream_t stream) {
     return mm_fn(x.codes(), x.scale(), w.codes(), w.scale(), out.data_ptr(), code_of(out.scalar_type()), x.r, w.r, x.k,
-                 stream);
+                 splits, stream);
   });
   return rc != FI_OK ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
 
-// (Aq, Ascale, Gq, Gscale, Uq, Uscale, out, out_dtype)
+// (Aq, Ascale, Gq, Gscale, Uq, Uscale, out, out_dtype, splits)
 PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Operand x, g, u;
   at::Tensor out;
-  if (n != 8 || !x.get(a[0], a[1], 1) || !g.get(a[2], a[3], kBlock) || !u.get(a[4], a[5], kBlock) || g.k != x.k ||
+  int splits;
+  if (n != 9 || !number(a[8], &splits) || !x.get(a[0], a[1], 1) || !g.get(a[2], a[3], kBlock) || !u.get(a[4], a[5], kBlock) || g.k != x.k ||
       u.k != x.k || u.r != g.r || g.q->get_device() != x.q->get_device() || u.q->get_device() != x.q->get_device() ||
       !output(a[6], a[7], x.r, g.r, x.q->get_device(), &out))
     Py_RETURN_NONE;
   const int rc = call(x.q->get_device(), [&](fi_stream_t stream) {
     return gated_fn(x.codes(), x.scale(), g.codes(), g.scale(), u.codes(), u.scale(), out.data_ptr(),
-                    code_of(out.scalar_type()), x.r, g.r, x.k, stream);
+                    code_of(out.scalar_type()), x.r, g.r, x.k, splits, stream);
   });
   return rc != FI_OK ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS
@@ -171,11 +182,9 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* z = n == 3 ? cuda_tensor(a[0]) : nullptr;
   const at::Tensor* tokens = z ? dense(a[1], at::kLong, 1) : nullptr;
   const int code = z ? code_of(z->scalar_type()) : -1;
-  if (!tokens || code < 0 || z->dim() != 2 || !PyLong_Check(a[2])) Py_RETURN_NONE;
-  int overflow = 0;
-  const long asked = PyLong_AsLongAndOverflow(a[2], &overflow);
-  // what is out of range stays so for the library to refuse
-  const int topk = overflow || asked < 0 || asked > FI_LOGPROBS_MAX_TOPK ? -1 : (int)asked;
+  int topk;
+  if (!tokens || code < 0 || z->dim() != 2 || !number(a[2], &topk)) Py_RETURN_NONE;
+  if (topk > FI_LOGPROBS_MAX_TOPK) topk = -1;  // before the outputs are made
   const int64_t rows = z->size(0), vocab = z->size(1), ld = rows <= 1 ? vocab : z->stride(0);
   const int device = z->get_device();
   if ((vocab > 1 && z->stride(1) != 1) || ld < vocab ||
@@ -200,7 +209,7 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The addresses of fi_fp8_quantize, fi_fp8_pack_weights, fi_mm_fp8, fi_mm_fp8_gated and
+// The addresses of fi_fp8_quantize, fi_fp8_pack_weights, fi_mm_fp8_ex, fi_mm_fp8_gated_ex and
 // fi_token_logprobs in the library that is loaded.
 PyObject* bind(PyObject*, PyObject* args) {
   unsigned long long f[5];

@@ -46,7 +46,7 @@ constexpr uint32_t kTileBytes = kTileRows * 128;   // a tile of one k block
 constexpr int kGroup = 4, kGroups = 2;             // blocks of k whose scales share a barrier; groups in the ring
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi0 = 3;
 constexpr int kMaxStages = 10, kMaxBufs = 4;
-constexpr int kMaxSplits = 8;                      // CTAs of a portable cluster
+constexpr int kMaxSplits = kFp8MaxSplits;
 
 // The geometry of one instance: N activation rows per tile, one weight tile or two (gated).
 template <int N, bool GATED>
@@ -369,7 +369,7 @@ struct Cut {
 // writes (of the gated N = 128, whose splits have twice as much to read from one another, half of that and
 // 0.2 us a split); up to 96 rows a wave's start and end count as 7 us.
 template <int N, bool GATED>
-int cut_tiles(const Fp8MmArgs& a, Cut* out) {
+int cut_tiles(const Fp8MmArgs& a, int splits, Cut* out) {
   using G = Geo<N, GATED>;
   const int sms = device_sm_count();
   auto kern = fp8_mm_kernel<N, GATED>;
@@ -411,7 +411,8 @@ int cut_tiles(const Fp8MmArgs& a, Cut* out) {
   const int64_t wrote = kMid ? std::min<int64_t>(a.m, N) * 8 / 10 : 0;
   out->units = (a.n + kTileRows - 1) / kTileRows * ((a.m + N - 1) / N);
   out->cost = -1;
-  for (int s = 1; s <= kMaxSplits && s <= a.kblocks; ++s) {
+  const int most = std::min(splits == 0 ? kMaxSplits : splits, a.kblocks);
+  for (int s = splits == 0 ? 1 : most; s <= most; ++s) {
     const int64_t at_once = active[dev][s];
     const int64_t cost =
         (out->units + at_once - 1) / at_once * ((a.kblocks + s - 1) / s * kBlock + kWave + (s > 1 && GATED && N == 128 ? wrote / 2 + 6 * s : wrote / s)) +
@@ -475,40 +476,41 @@ int64_t wide_cost(const Fp8MmArgs& a, bool gated) {
 //   gated from 65 rows on, tiles of 64 / 128 / CTA pairs: 128 of 65 x 11408 11.5 / 18.1 / 38.3, of
 //   1746 x 1136 8.6 / 10.7 / 9.2, of 17408 x 5120 53.9 / 44.5 / 45.5, 200 of 8192 x 2048 30.3 / 24.6 / 13.2.
 template <int N1, int N2, bool GATED>
-int launch_cheapest(const Fp8MmArgs& a, bool pair, cudaStream_t stream) {
+int launch_cheapest(const Fp8MmArgs& a, int splits, bool pair, cudaStream_t stream) {
   Cut one, two;
-  int rc = cut_tiles<N1, GATED>(a, &one);
-  if (rc == FI_OK) rc = cut_tiles<N2, GATED>(a, &two);
+  int rc = cut_tiles<N1, GATED>(a, splits, &one);
+  if (rc == FI_OK) rc = cut_tiles<N2, GATED>(a, splits, &two);
   if (rc != FI_OK) return rc;
   if (pair && wide_cost(a, GATED) < std::min(one.cost, two.cost)) return launch_fp8_wide(a, GATED, stream);
   return one.cost < two.cost ? launch_tile<N1, GATED>(a, one, stream) : launch_tile<N2, GATED>(a, two, stream);
 }
 
 template <int N, bool GATED>
-int launch_only(const Fp8MmArgs& a, cudaStream_t stream) {
+int launch_only(const Fp8MmArgs& a, int splits, cudaStream_t stream) {
   Cut cut;
-  const int rc = cut_tiles<N, GATED>(a, &cut);
+  const int rc = cut_tiles<N, GATED>(a, splits, &cut);
   return rc != FI_OK ? rc : launch_tile<N, GATED>(a, cut, stream);
 }
 
 }  // namespace
 
-int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream) {
+int launch_fp8_mm(Fp8MmArgs a, bool gated, int splits, cudaStream_t stream) {
   a.err = device_error_word();
   if (!a.err) return set_cuda_error("cudaGetSymbolAddress(device error word)");
   a.timeout_ns = wait_timeout_ns();
   a.debug_stall = take_debug_stall();
+  const bool pair = splits <= 1;  // the CTA-pair kernel has no splits
   if (gated) {
-    if (a.m <= 16) return launch_only<16, true>(a, stream);
-    if (a.m <= 32) return launch_only<32, true>(a, stream);
-    if (a.m <= 64) return launch_only<64, true>(a, stream);
-    return launch_cheapest<64, 128, true>(a, true, stream);
+    if (a.m <= 16) return launch_only<16, true>(a, splits, stream);
+    if (a.m <= 32) return launch_only<32, true>(a, splits, stream);
+    if (a.m <= 64) return launch_only<64, true>(a, splits, stream);
+    return launch_cheapest<64, 128, true>(a, splits, pair, stream);
   }
-  if (a.m <= 16) return launch_only<16, false>(a, stream);
-  if (a.m <= 32) return launch_only<32, false>(a, stream);
-  if (a.m <= 64) return launch_only<64, false>(a, stream);
-  if (a.m <= 96) return launch_cheapest<96, 128, false>(a, false, stream);
-  return launch_cheapest<128, 256, false>(a, a.m > 128, stream);
+  if (a.m <= 16) return launch_only<16, false>(a, splits, stream);
+  if (a.m <= 32) return launch_only<32, false>(a, splits, stream);
+  if (a.m <= 64) return launch_only<64, false>(a, splits, stream);
+  if (a.m <= 96) return launch_cheapest<96, 128, false>(a, splits, false, stream);
+  return launch_cheapest<128, 256, false>(a, splits, pair && a.m > 128, stream);
 }
 
 }  // namespace fi

@@ -205,7 +205,9 @@ struct Fp8MmArgs {
   unsigned* err;         // the device error word
   uint64_t timeout_ns;   // limit of every mbarrier wait
 };
-int launch_fp8_mm(Fp8MmArgs a, bool gated, cudaStream_t stream);
+constexpr int kFp8MaxSplits = 8;  // CTAs of a portable cluster
+// splits: K splits, 0 for as many as the sizes suggest.
+int launch_fp8_mm(Fp8MmArgs a, bool gated, int splits, cudaStream_t stream);
 // The CTA-pair kernel for many activation rows (launch_fp8_mm decides).
 int launch_fp8_wide(Fp8MmArgs a, bool gated, cudaStream_t stream);
 

@@ -301,7 +301,9 @@ FI_API int fi_fp8_pack_weights(const void* W, int dtype, int64_t n, int64_t k, u
  * product of their two scales, are added in fp32 in order of k (K splits, where a call takes
  * them, are added in order after that); one rounding to out_dtype (FI_DTYPE_BF16, FI_DTYPE_F16
  * with +-inf from 65520 on, or FI_DTYPE_F32). Results repeat bit for bit from run to run. How many
- * K splits a call takes depends on its sizes, so a row's last bits may depend on m.
+ * K splits a call takes depends on its sizes, so a row's last bits may depend on m and n; fi_mm_fp8_ex
+ * fixes them. The product of two scales is itself rounded to fp32: scales whose product leaves its normal
+ * range give sums that are off.
  *   Aq, Ascale  activations as written by fi_fp8_quantize; Aq 16-byte aligned.
  *   Wq, Wscale  weights as written by fi_fp8_pack_weights; Wq 16-byte aligned.
  *   out         device [m, n] of out_dtype; must not overlap the inputs.
@@ -309,6 +311,18 @@ FI_API int fi_fp8_pack_weights(const void* W, int dtype, int64_t n, int64_t k, u
  */
 FI_API int fi_mm_fp8(const uint8_t* Aq, const float* Ascale, const uint8_t* Wq, const float* Wscale, void* out,
               int out_dtype, int64_t m, int64_t n, int64_t k, fi_stream_t stream);
+
+/*
+ * fi_mm_fp8 with the number of K splits given: FI_FP8_MAX_SPLITS at most, of which no more are taken than
+ * there are blocks of k; 0 leaves it to the library. With a number given, the order of the additions follows
+ * from it and k alone, and the bits of an output from its row of A and of W: not from m, n or the
+ * kernel that the sizes select. 1 is the number for prompts, since with more the kernel for many rows is not
+ * taken (4096 x 4096 x 4096: 65 us with 1, 148 with 2); a decode call of few weight rows wants 4 to 8
+ * (1 x 4096 x 14336: 37.5 us with 1, 10.2 with 8).
+ */
+#define FI_FP8_MAX_SPLITS 8
+FI_API int fi_mm_fp8_ex(const uint8_t* Aq, const float* Ascale, const uint8_t* Wq, const float* Wscale, void* out,
+                 int out_dtype, int64_t m, int64_t n, int64_t k, int splits, fi_stream_t stream);
 
 /*
  * The first half of a gated feed-forward block in one kernel:
@@ -321,6 +335,11 @@ FI_API int fi_mm_fp8(const uint8_t* Aq, const float* Ascale, const uint8_t* Wq, 
 FI_API int fi_mm_fp8_gated(const uint8_t* Aq, const float* Ascale, const uint8_t* Gq, const float* Gscale,
                     const uint8_t* Uq, const float* Uscale, void* out, int out_dtype, int64_t m,
                     int64_t n, int64_t k, fi_stream_t stream);
+
+/* fi_mm_fp8_gated with the number of K splits given, as fi_mm_fp8_ex. */
+FI_API int fi_mm_fp8_gated_ex(const uint8_t* Aq, const float* Ascale, const uint8_t* Gq, const float* Gscale,
+                       const uint8_t* Uq, const float* Uscale, void* out, int out_dtype, int64_t m,
+                       int64_t n, int64_t k, int splits, fi_stream_t stream);
 
 /* ------------------------------------------------------------ token log probabilities */
 
