@@ -49,6 +49,7 @@ TACTIC_DEFAULT = -1
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 # element types of the 8-bit products' inputs and outputs and of the logits
 _DTYPES_ANY = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_MAX_M = 256     # activation rows of an NVFP4 product
 FP8_BLOCK = 128  # k (and weight rows) per scale
 MAX_TOPK = 32    # FI_LOGPROBS_MAX_TOPK
 MAX_FP8_SPLITS = 8  # FI_FP8_MAX_SPLITS
@@ -537,11 +538,19 @@ def lm_head_logprobs(A: torch.Tensor, weight: tuple, tokens: torch.Tensor, topk:
     """What a server answers with: the lm_head product of the last hidden states A [rows, k]
     (bf16) and the log probabilities of one token per row. `weight` is an 8-bit head (Wq, Wscale)
     of pack_weights_fp8, whose logits stay in fp32, or an NVFP4 head (Wq, Wscale, gscale) of
-    pack_weights, whose logits are bf16 (at most 256 rows, as mm_bf16_fp4)."""
-    if len(weight) == 3:
-        logits = mm_bf16_fp4(A, *weight)
-    elif len(weight) == 2:
-        logits = mm_fp8(*quantize_fp8(A), *weight, out_dtype=torch.float32)
-    else:
+    pack_weights, whose logits are bf16. An NVFP4 head takes 256 rows at a time, as many as
+    mm_bf16_fp4; an 8-bit head's logits are held all at once."""
+    if len(weight) == 2:
+        return token_logprobs(mm_fp8(*quantize_fp8(A), *weight, out_dtype=torch.float32), tokens, topk)
+    if len(weight) != 3:
         raise ValueError("weight must be (Wq, Wscale) of pack_weights_fp8 or (Wq, Wscale, gscale) of pack_weights")
-    return token_logprobs(logits, tokens, topk)
+    _require(A, "A", torch.bfloat16, 2)
+    rows = A.shape[0]
+    if rows <= _MAX_M:
+        return token_logprobs(mm_bf16_fp4(A, *weight), tokens, topk)
+    _require(tokens, "tokens", torch.int64, 1)
+    if tokens.shape[0] != rows:
+        raise ValueError(f"tokens must be [{rows}], got {tuple(tokens.shape)}")
+    parts = [token_logprobs(mm_bf16_fp4(A[i:i + _MAX_M], *weight), tokens[i:i + _MAX_M], topk)
+             for i in range(0, rows, _MAX_M)]
+    return TokenLogprobs(*(torch.cat(f) for f in zip(*parts)))
