@@ -90,7 +90,8 @@ bool output(PyObject* out, PyObject* dtype, int64_t m, int64_t n, int device, at
 template <typename F>
 int call(int device, F fn) {
   const c10::cuda::OptionalCUDAGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)device));
-  const fi_stream_t stream = reinterpret_cast<fi_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+  const fi_stream_t stream =
+      reinterpret_cast<fi_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = fn(stream);
@@ -164,8 +165,8 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Operand x, g, u;
   at::Tensor out;
   int splits;
-  if (n != 9 || !number(a[8], &splits) || !x.get(a[0], a[1], 1) || !g.get(a[2], a[3], kBlock) || !u.get(a[4], a[5], kBlock) || g.k != x.k ||
-      u.k != x.k || u.r != g.r || g.q->get_device() != x.q->get_device() || u.q->get_device() != x.q->get_device() ||
+  if (n != 9 || !number(a[8], &splits) || !x.get(a[0], a[1], 1) || !g.get(a[2], a[3], kBlock) ||
+      !u.get(a[4], a[5], kBlock) || g.k != x.k || u.k != x.k || u.r != g.r || g.q->get_device() != x.q->get_device() || u.q->get_device() != x.q->get_device() ||
       !output(a[6], a[7], x.r, g.r, x.q->get_device(), &out))
     Py_RETURN_NONE;
   const int rc = call(x.q->get_device(), [&](fi_stream_t stream) {

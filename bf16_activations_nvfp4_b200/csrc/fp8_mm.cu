@@ -362,12 +362,28 @@ struct Cut {
   int64_t cost;
 };
 
-// The split of least cost: waves of clusters, each with its blocks of k, a start and an end, and the
-// meeting of a cluster. Measured on B200: a block of N = 256 rows takes 0.72 us, one of the gated
-// N = 128 0.9 us, of the gated N = 64 0.4 us, one of N = 128 0.37 us, one of N = 96 with two CTAs on
-// every SM 0.65 us; a wave's start and end 5.2 us (the gated N = 64: 6.7) and 0.03 us per row that a CTA
-// writes (of the gated N = 128, whose splits have twice as much to read from one another, half of that and
-// 0.2 us a split); up to 96 rows a wave's start and end count as 7 us.
+// What a tile of N activation rows takes, as measured on B200 (a tenth of a block of the CTA-pair kernel is
+// 36 ns): a block of k; a wave's start and end; for each row that a CTA writes, in tenths. A wave of a
+// tile that competes with no other counts 7 us, its writing included.
+struct TileCost {
+  int block, wave, row;
+};
+template <int N, bool GATED>
+constexpr TileCost tile_cost() {
+  if constexpr (GATED) {
+    if (N == 128) return {24, 145, 8};  // 0.9 us a block, 5.2 us a wave, 0.03 us a row
+    if (N == 64) return {11, 185, 8};   // 0.4, 6.7
+  } else {
+    if (N == 256) return {20, 145, 8};  // 0.72, 5.2
+    if (N == 128) return {10, 145, 8};  // 0.37, 5.2
+    if (N == 96) return {18, 200, 0};   // 0.65 with two CTAs on every SM
+  }
+  return {9, 200, 0};
+}
+
+// The split of least cost, or the given one: waves of clusters, each with its blocks of k, a start and
+// an end, and the meeting of a cluster (1.4 us). The gated N = 128, whose splits have twice as much
+// to read from one another, writes half of its rows' cost whatever the split, and 0.2 us a split.
 template <int N, bool GATED>
 int cut_tiles(const Fp8MmArgs& a, int splits, Cut* out) {
   using G = Geo<N, GATED>;
@@ -405,18 +421,17 @@ int cut_tiles(const Fp8MmArgs& a, int splits, Cut* out) {
     }
     active[dev][0] = 1;
   }
-  constexpr bool kMid = N >= 128 || (GATED && N == 64);  // tiles that compete with one another
-  constexpr int64_t kBlock = N == 256 ? 20 : (GATED && N == 128 ? 24 : (N == 96 ? 18 : (GATED && N == 64 ? 11 : (N == 128 ? 10 : 9))));
-  constexpr int64_t kWave = !kMid ? 200 : (N == 64 ? 185 : 145);
-  const int64_t wrote = kMid ? std::min<int64_t>(a.m, N) * 8 / 10 : 0;
+  constexpr TileCost kCost = tile_cost<N, GATED>();
+  constexpr bool kTwice = GATED && N == 128;
+  const int64_t rows = std::min<int64_t>(a.m, N) * kCost.row / 10;
   out->units = (a.n + kTileRows - 1) / kTileRows * ((a.m + N - 1) / N);
   out->cost = -1;
   const int most = std::min(splits == 0 ? kMaxSplits : splits, a.kblocks);
   for (int s = splits == 0 ? 1 : most; s <= most; ++s) {
     const int64_t at_once = active[dev][s];
-    const int64_t cost =
-        (out->units + at_once - 1) / at_once * ((a.kblocks + s - 1) / s * kBlock + kWave + (s > 1 && GATED && N == 128 ? wrote / 2 + 6 * s : wrote / s)) +
-        (s > 1 ? 40 : 0);
+    const int64_t write = s > 1 && kTwice ? rows / 2 + 6 * s : rows / s;
+    const int64_t wave = (a.kblocks + s - 1) / s * kCost.block + kCost.wave + write;
+    const int64_t cost = (out->units + at_once - 1) / at_once * wave + (s > 1 ? 40 : 0);
     if (out->cost < 0 || cost < out->cost) {
       out->cost = cost;
       out->splits = s;
@@ -454,7 +469,8 @@ int launch_tile(Fp8MmArgs a, const Cut& cut, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, fp8_mm_kernel<N, GATED>, a, ta, tw[0], tw[1]) != cudaSuccess) return set_cuda_error("fp8_mm_kernel launch");
+  if (cudaLaunchKernelEx(&cfg, fp8_mm_kernel<N, GATED>, a, ta, tw[0], tw[1]) != cudaSuccess)
+    return set_cuda_error("fp8_mm_kernel launch");
   return FI_OK;
 }
 

@@ -21,12 +21,6 @@ namespace fi {
 
 namespace {
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // Two fp32 values to two E4M3 codes (low byte = lo), round to nearest even, saturating.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   unsigned short r;
@@ -94,18 +88,6 @@ struct Vec<FI_DTYPE_F16> {
   }
 };
 
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-  return d;
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 // A block's scale and what its divisions need. Where the scale is far from the ends of the fp32
 // range, x / scale is found as Markstein's theorem allows ("Computation of elementary functions on
 // the IBM RISC System/6000 processor", 1990): with y the correctly rounded reciprocal and q within
@@ -131,12 +113,11 @@ __device__ __forceinline__ Scale block_scale(float amax) {
 
 __device__ __forceinline__ uint32_t quotient_codes(float x0, float x1, const Scale& s) {
   const uint64_t x = pack2(x0, x1);
-  uint64_t q;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(s.my));
+  uint64_t q = mul2(x, s.my);
   q = fma2(fma2(q, s.ss, x), s.my, q);
   q = fma2(fma2(q, s.ss, x), s.my, q);
   float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(q));
+  unpack2(q, lo, hi);
   return f32x2_to_e4m3x2(lo, hi);  // of the negative quotients
 }
 
@@ -171,9 +152,9 @@ __device__ __forceinline__ void store_codes(const uint4 v, const Scale& s, uint8
 // lane so that U loads are in flight. WHOLE: k is a multiple of 128, so that the groups follow one
 // another in memory and no row has to be found.
 template <int DT, int U, bool WHOLE>
-__global__ void __launch_bounds__(256, DT == FI_DTYPE_F32 ? 4 : 6) fp8_quant_rows_kernel(const uint8_t* __restrict__ x, int64_t groups,
-                                                             uint32_t kblocks, int64_t k, uint8_t* __restrict__ q,
-                                                             float* __restrict__ scale) {
+__global__ void __launch_bounds__(256, DT == FI_DTYPE_F32 ? 4 : 6)
+    fp8_quant_rows_kernel(const uint8_t* __restrict__ x, int64_t groups, uint32_t kblocks, int64_t k,
+                          uint8_t* __restrict__ q, float* __restrict__ scale) {
   constexpr int kN = Vec<DT>::kN, kLanes = kFp8Block / kN, kEs = 16 / kN;
   pdl_launch_dependents();
   pdl_wait();
@@ -208,9 +189,9 @@ __global__ void __launch_bounds__(256, DT == FI_DTYPE_F32 ? 4 : 6) fp8_quant_row
 
 // One CTA of 512 threads per 128 x 128 block, 32 elements per thread.
 template <int DT>
-__global__ void __launch_bounds__(512, DT == FI_DTYPE_F32 ? 2 : 4) fp8_quant_square_kernel(const uint8_t* __restrict__ x, int64_t rows,
-                                                               uint32_t kblocks, int64_t k, uint8_t* __restrict__ q,
-                                                               float* __restrict__ scale) {
+__global__ void __launch_bounds__(512, DT == FI_DTYPE_F32 ? 2 : 4)
+    fp8_quant_square_kernel(const uint8_t* __restrict__ x, int64_t rows, uint32_t kblocks, int64_t k,
+                            uint8_t* __restrict__ q, float* __restrict__ scale) {
   constexpr int kN = Vec<DT>::kN, kLanes = kFp8Block / kN, kEs = 16 / kN, kU = 32 / kN;
   pdl_launch_dependents();
   pdl_wait();

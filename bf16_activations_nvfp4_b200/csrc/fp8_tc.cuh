@@ -158,26 +158,6 @@ __device__ __forceinline__ void store_out4(void* out, int dtype, int64_t at, flo
   if (left > 3) store_out(out, dtype, at + 3, v.w);
 }
 
-// Packed pairs of fp32: one instruction for two.
-__device__ __forceinline__ uint64_t pair_of(float x, float y) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-  return d;
-}
-__device__ __forceinline__ void pair_to(uint64_t v, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 // (a, b) = (silu(a) u, silu(b) v) with silu(g) = g / (1 + exp(-g)) through e = exp(-|g|), which cannot overflow:
 // g e / (1 + e) where g < 0. The activation is off by at most 7 units (2^-23) of itself for every g, and by
 // a few of 2^-149 where it is subnormal. e is 2^t corrected by what t = -|g| log2 e lost in its rounding, as it is
@@ -187,21 +167,21 @@ __device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c)
 __device__ __forceinline__ void silu_times(float& a, float& b, float u, float v) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   constexpr float kLn2Rest = (float)(0.6931471805599453 - (double)kLn2);
-  const uint64_t x = pair_of(fmaxf(-fabsf(a), -200.0f), fmaxf(-fabsf(b), -200.0f));
-  const uint64_t t = pair_mul(x, pair_of(kLog2e, kLog2e));
-  const uint64_t lost = pair_fma(t, pair_of(-kLn2Rest, -kLn2Rest), pair_fma(t, pair_of(-kLn2, -kLn2), x));
+  const uint64_t x = pack2(fmaxf(-fabsf(a), -200.0f), fmaxf(-fabsf(b), -200.0f));
+  const uint64_t t = mul2(x, pack2(kLog2e, kLog2e));
+  const uint64_t lost = fma2(t, pack2(-kLn2Rest, -kLn2Rest), fma2(t, pack2(-kLn2, -kLn2), x));
   float t0, t1, e0, e1, d0, d1, r0, r1;
-  pair_to(t, t0, t1);
+  unpack2(t, t0, t1);
   const bool far0 = t0 < -64.0f, far1 = t1 < -64.0f;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(far0 ? t0 + 64.0f : t0));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(far1 ? t1 + 64.0f : t1));
-  const uint64_t e2 = pair_of(e0, e1), e = pair_fma(e2, lost, e2);
-  const uint64_t back = pair_of(far0 ? 0x1p-64f : 1.0f, far1 ? 0x1p-64f : 1.0f);
-  pair_to(pair_fma(e, back, pair_of(1.0f, 1.0f)), d0, d1);
+  const uint64_t e2 = pack2(e0, e1), e = fma2(e2, lost, e2);
+  const uint64_t back = pack2(far0 ? 0x1p-64f : 1.0f, far1 ? 0x1p-64f : 1.0f);
+  unpack2(fma2(e, back, pack2(1.0f, 1.0f)), d0, d1);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
-  pair_to(pair_mul(pair_mul(pair_of(a, b), e), back), d0, d1);
-  pair_to(pair_mul(pair_mul(pair_of(a < 0.0f ? d0 : a, b < 0.0f ? d1 : b), pair_of(r0, r1)), pair_of(u, v)), a, b);
+  unpack2(mul2(mul2(pack2(a, b), e), back), d0, d1);
+  unpack2(mul2(mul2(pack2(a < 0.0f ? d0 : a, b < 0.0f ? d1 : b), pack2(r0, r1)), pack2(u, v)), a, b);
 }
 
 // Codes [rows, k] in boxes of 128 k x box_rows, 128-byte swizzle; what is outside reads as zero.

@@ -22,7 +22,7 @@
 // meet in distributed shared memory. No workspace, no atomics.
 //
 // 2047 x 152064 bf16 takes 99 us without token or list (6.3 TB/s), 117 with ranks, 147 with 5
-// alternatives, 212 with 32: bound by HBM, then by instruction issue (61% of the slots, at 14 warps
+// alternatives, 212 with 32: bound by HBM, then by instruction issue (73% of the slots, at 24 warps
 // per SM) and the latency of the lists' steps, during which a warp's next groups are on their way to
 // shared memory (held in registers instead, one group ahead, and candidates inserted one by one it
 // was 111, 131, 186 and 262). 1024 x 152064 fp32 with 5 takes 122 us, 4096 x 32000 bf16 with 5 89
@@ -56,12 +56,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -0x1p26f;  // stands for -inf and all below it (0xCC80 in bf16)
 constexpr float kFarMax = 0x1p24f;  // a greater magnitude of the row's maximum takes a second pass
 constexpr float kFar = -1e30f;    // least difference of two maxima: times a sum it stays finite
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float d;
@@ -118,9 +112,9 @@ __device__ __forceinline__ uint32_t word_of(const uint32_t (&w)[4], int i) {
   return i & 2 ? hi : lo;
 }
 
-// kN elements in four 32-bit words; get and pick: element i (pick: i not known at compile time). raw: one element and masked ones in a word; wmax: the greater of two words, element by element; lift: the
-// word with its -inf replaced by a value whose exponential is 0 (for f16, once it is fp32);
-// count: n += the word's elements above those of `limit` (NaN is above everything).
+// kN elements in four 32-bit words; get and pick: element i (pick: i not known at compile time); raw: one
+// element and masked ones in a word; wmax: the greater of two words, element by element; lift: the word
+// with its -inf replaced by a value whose exponential is 0 (for f16, once it is fp32); count: n += the word's elements above those of `limit` (NaN is above everything).
 template <int DT>
 struct Elem;
 template <>
@@ -208,26 +202,6 @@ struct Elem<FI_DTYPE_F16> {
   }
   __device__ static uint32_t counted(uint32_t n) { return (uint32_t)(f16_lo_to_f32(n) + f16_hi_to_f32(n)); }
 };
-
-// Packed pairs of fp32: one instruction for two elements.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 
 // Sums relative to a reference point M = m log2 e (rounded to fp32, the same wherever it is
 // formed from m): s = sum of 2^(z log2 e - M), t = sum of (z log2 e - M) times that.

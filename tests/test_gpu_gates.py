@@ -1,4 +1,6 @@
 """The gated product's activation on exact gates, over the whole range of the exponential."""
+import math
+
 import pytest
 import torch
 
@@ -61,7 +63,20 @@ def test_exact_gates(m, n, dtype):
 
 
 def test_gates_without_end():
-    """Gates that are infinite or NaN, as the formula has them: g / (1 + exp(-g))."""
+    """Gates that are infinite or NaN, as the formula has them: g / (1 + exp(-g)) u, here with u = g."""
+    inf = float("inf")
+    a, g, _ = _operands(torch.tensor([inf, -inf, float("nan"), 1.0, 3e38, -3e38]), torch.ones(5))
+    u = (g[0], g[1].clone())
+    u[1][:] = 2.0 ** -120
+    out = fi.mm_fp8_gated(*_fp8.cuda(a), *_fp8.cuda(g), *_fp8.cuda(u), out_dtype=torch.float32).cpu()
+    assert bool((out[0] == inf).all()) and bool(torch.isnan(out[1:3]).all())
+    silu = 1 / (1 + math.exp(-1))
+    assert bool(torch.isclose(out[3], torch.tensor(silu * 2.0 ** -120), rtol=2.0 ** -20, atol=0).all())
+    assert bool((out[4] == inf).all())  # 3e38 times 226
+    assert bool((out[5] == 0).all())
+
+
+def test_up_values_without_end_stay_in_their_rows():
     inf = float("inf")
     a, g, u = _operands(torch.tensor([inf, -inf, float("nan"), 1.0]), torch.ones(5))
     a[1][3, 0] = 3e38
