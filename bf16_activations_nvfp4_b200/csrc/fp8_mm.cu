@@ -130,6 +130,8 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_slot;
+  // waited for before the first access to another CTA's shared memory: they have all started
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_launch_dependents();
 
   if (warp == kWarpTma) {
@@ -299,18 +301,22 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
 
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();
+  // Where a wait of any CTA of the cluster ran out, the sums are not the blocks': nothing is stored. The CTA
+  // that gave up tells the others. (Read from them by each warp, the flags took 0.25 us of the 9.8 of
+  // 64 x 5120 x 5120; a mark in the sums took as much.)
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (abort_flag)
+    for (int r = 0; r < S; ++r) st_dsmem_u32(const_cast<int*>(&abort_flag), (uint32_t)r, 1);
+  __syncwarp();
   cluster_sync();
-  // where a wait of any CTA of the cluster ran out, the sums are not the blocks': nothing is stored
-  const int mine = lane < S ? (int)ld_dsmem_u32(const_cast<const int*>(&abort_flag), (uint32_t)lane) : 0;
+  const bool sound = abort_flag == 0;
   // four outputs of one activation row at a time: all splits' sums are on their way before the
   // first is added
   const int quads = rows * (kTileRows / 4);
   const int chunk = (quads + S - 1) / S;
   const int q_end = min(quads, (split + 1) * chunk);
   const bool wide = p.n % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
-  bool sound = true;
-  for (int e0 = split * chunk + warp * 32; e0 < q_end; e0 += G::kThreads) {
-    const int e = min(e0 + lane, q_end - 1);  // the last ones read what they do not store
+  for (int e = split * chunk + (int)threadIdx.x; e < q_end; e += G::kThreads) {
     const int64_t j = tile_n * kTileRows + (e & (kTileRows / 4 - 1)) * 4;
     float4 v[G::kTiles];
 #pragma unroll
@@ -320,7 +326,6 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
 #pragma unroll
       for (int r = 0; r < kMaxSplits; ++r)
         if (r < S) part[r] = ld_dsmem_v4(at, (uint32_t)r);
-      if (t == 0) sound = !__any_sync(0xffffffffu, mine != 0);
       v[t] = part[0];
 #pragma unroll
       for (int r = 1; r < kMaxSplits; ++r) {
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(Geo<N, GATED>::kThreads, Geo<N, GATED>::kCtas)
       silu_times(v[0].x, v[0].y, u.x, u.y);
       silu_times(v[0].z, v[0].w, u.z, u.w);
     }
-    if (sound && e0 + lane < q_end && j < p.n)
+    if (sound && j < p.n)
       store_out4(p.out, p.out_dtype, (m0 + e / (kTileRows / 4)) * p.n + j, v[0], wide, p.n - j);
   }
   __syncwarp();

@@ -69,6 +69,11 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The word at `p` (shared memory of this CTA) in the cluster's CTA `rank`.
+__device__ __forceinline__ void st_dsmem_u32(void* p, uint32_t rank, uint32_t v) {
+  uint32_t remote;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
   uint32_t remote, v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(p)), "r"(rank));
