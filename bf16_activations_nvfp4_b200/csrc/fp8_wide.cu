@@ -21,9 +21,8 @@
 // Bound by the chain of a block's steps (MMAs, commit, TMEM loads, additions, release: two TMEM
 // buffers are in flight) and, under sustained load, by power: 720 to 750 cycles per block of a pair
 // where the MMAs and loads alone take 638 and the nominal rate is 512. 8192 x 4096 x 14336 takes
-// 404 us (2.4 PFLOP/s), 470 at the power limit; 4096 rows of the gated 2 x 17408 x 5120 617 us in 20
-// calls, 721 at the power limit.
-// N = 128 instructions with four buffers took 646 us on the former where this form took 504, 16
+// 404 us (2.4 PFLOP/s), 470 at the power limit; 4096 rows of the gated 2 x 17408 x 5120 617 us, 730
+// at the power limit. N = 128 instructions with four buffers took 646 us on the former where this form took 504, 16
 // epilogue warps 559 against 450.
 //
 // Every wait is bounded; on a timeout the roles stop and every thread still meets the barriers.

@@ -358,7 +358,8 @@ FI_API int fi_mm_fp8_gated_ex(const uint8_t* Aq, const float* Ascale, const uint
  * No logprob is above 0 and no entropy below; a row with one entry left has 0 for both.
  * An entry of -inf is masked: it has probability 0 and adds nothing. A row of nothing else has
  * logprob -inf and entropy 0. A row that holds NaN or +inf has NaN logprob and entropy; NaN comes
- * first in the order. A token outside [0, vocab) has logprob NaN and rank -1.
+ * first in the order. A token outside [0, vocab) has logprob NaN and rank -1. Results repeat bit for
+ * bit; how many threads share a row depends on the number of rows, and so may the sums' last bits.
  * Preconditions: rows >= 0, vocab >= 1, 0 <= topk <= FI_LOGPROBS_MAX_TOPK. rows == 0 is a no-op.
  */
 #define FI_LOGPROBS_MAX_TOPK 32
@@ -409,7 +410,9 @@ FI_API int fi_set_workspace(void* ptr, size_t bytes);
 
 /* Read and clear the current device's sticky kernel error word (0 = no error): bit 0 a
  * consumer (decode) wait, bit 1 a producer wait, bit 2 a final drain, bit 3 (MMA) a drain
- * before exit, bit 4 (MMA) the epilogue's wait ran out. Synchronizes the device. */
+ * before exit, bit 4 (MMA) the epilogue's wait ran out. The limit counts from the end of the kernel that
+ * precedes the call on its stream. After an error the outputs of the call are undefined; the 8-bit products
+ * leave those whose sums did not come about as they were. Synchronizes the device. */
 FI_API int fi_get_device_error(unsigned* code);
 
 /* Test hooks. FI_DEBUG_STALL_PRODUCER: the producers of the next `value` launches (the ring
