@@ -31,7 +31,7 @@ def test_launches_of_several_threads_are_counted_once():
         except Exception as e:  # an assertion in a thread is not seen
             wrong.append(repr(e))
 
-    fi.debug_set(fi.DEBUG_WAIT_TIMEOUT_NS, 200_000)
+    fi.debug_set(fi.DEBUG_WAIT_TIMEOUT_NS, 1_000_000)
     fi.debug_set(fi.DEBUG_STALL_PRODUCER, stalled)
     try:
         workers = [threading.Thread(target=work, args=(o,)) for o in outs]
